@@ -327,6 +327,99 @@ nq_status nq_binary_matmul(const uint32_t *U_packed, const uint32_t *V_packed, c
                            nq_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
+/* 4. Layers with 4-bit weights.  Below one bit is not for every layer (summary */
+/* page, "Limitations" (局限与改进)): heads, sensitive projections and experts    */
+/* are kept at 4 bits beside the binary factors, quantised with the same         */
+/* calibration (d_in) and applied to one token or to a prompt.                   */
+/*                                                                               */
+/* Format of an m x n layer with group size g (32, 64 or 128):                    */
+/*   packed uint32 [m][4 ceil(n/32)]: the code q of column k is nibble k % 8      */
+/*     (lowest first) of word k / 8 of its row; codes past column n are ignored;   */
+/*   scales bf16 [m][ceil(n/g)]; zeros uint8 [m][ceil(n/g)] (0..15), or NULL for   */
+/*     a zero point of 8 everywhere;                                              */
+/*   W^[i][k] = scale (q - zero), exact in FP32.                                  */
+/* Supported sizes: 1 <= n <= 65536, 1 <= m <= 2^24 (a stack of layers is one      */
+/* array of rows).  packed starts on a 16-byte boundary.                           */
+/* ------------------------------------------------------------------------- */
+
+/* Most candidates of the quantiser's clipping search. */
+#define NQ_W4_MAX_GRID 64
+
+/*
+ * Quantise W (device, m x n, dtype dt).  Per row and group, for c = 0 .. grid - 1 with
+ * alpha = 1 - c / (2 grid):
+ *   zeros NULL:  s = bf16(alpha max|w| / 7), z = 8
+ *   else:        lo = min(0, min w), hi = max(0, max w), s = bf16(alpha (hi - lo) / 15),
+ *                z = clamp(rint(-alpha lo / s), 0, 15)
+ *   q = clamp(rint(w / s) + z, 0, 15)
+ *   E = sum_j d_in_j^2 (w_j - s (q_j - z))^2
+ * and the lowest c with the least E is kept (grid 1: rounding to nearest without clipping).
+ * Scales are formed in FP64 and rounded to FP32, then BF16; w / s is rounded as the exact
+ * quotient (ties to even); E is compared in FP64.  s = 0 gives q = z (z = 0 with zeros).
+ * d_in: device float (n), as nq_calib_precond gives it, or NULL for 1.  A group that holds
+ * an infinite or NaN weight gets the scale NaN (it reads back as NaN; other groups are as
+ * without it).  packed, scales, zeros: device, all written.  Enqueue only.
+ */
+nq_status nq_w4_quantize(const void *W, nq_dtype dt, int64_t m, int64_t n, const float *d_in,
+                         int32_t group, int32_t grid, uint32_t *packed, void *scales,
+                         uint8_t *zeros, nq_stream_t stream);
+
+/* Read back: W^ (device, m x n, dtype dt; FP32 exact, BF16 rounded to nearest).  Enqueue
+ * only. */
+nq_status nq_w4_dequantize(const uint32_t *packed, const void *scales, const uint8_t *zeros,
+                           int64_t m, int64_t n, int32_t group, void *W, nq_dtype dt,
+                           nq_stream_t stream);
+
+/* Workspace bytes of nq_w4_matmul for B rows of X of dtype dt (0: the call takes no
+ * workspace, or the sizes are out of range). */
+size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
+
+/*
+ * Y = X W^^T:  Y[b][i] = sum_k W^[i][k] X[b][k] for B <= 65536 rows of X.
+ *   X [B][n] (dtype dt, row stride n), Y [B][m] float: device.
+ * The integers q - z and the activations (BF16, or FP32 as three BF16 terms that sum to it
+ * exactly) are multiplied exactly, summed in FP32 within a group, scaled in FP32 and summed
+ * in FP32 over the groups in a fixed order: the result of a row of X does not depend on
+ * the run.  An infinite or NaN activation reaches its own row of Y alone.  Enqueue only.
+ */
+nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,
+                       int64_t n, int32_t group, const void *X, nq_dtype dt, int64_t B, float *Y,
+                       void *ws, size_t ws_bytes, nq_stream_t stream);
+
+/* Limits of nq_moe_w4. */
+#define NQ_MOE_MAX_TOKENS 64
+#define NQ_MOE_MAX_EXPERTS 512
+#define NQ_MOE_MAX_TOP_K 16
+
+/* Workspace bytes of nq_moe_w4 (0 for sizes out of range). */
+size_t nq_moe_workspace_size(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k,
+                             nq_dtype dt);
+
+/*
+ * A mixture-of-experts layer for B <= NQ_MOE_MAX_TOKENS tokens:
+ *   l_e = sum_k router[e][k] x_k;  the top_k largest l_e are chosen (ties: the lowest e);
+ *   p_e = exp(l_e) / sum of exp(l) over all experts, or over the chosen ones (renormalise);
+ *   y = sum over the chosen e of p_e Down_e (silu(Gate_e x) * (Up_e x)),
+ *   silu(v) = v / (1 + exp(-v)).
+ *   X [B][d], router [E][d] (dtype dt): device.
+ *   gate_up: E matrices of 2f x d in the packed format one after the other, rows 0..f-1 the
+ *     gate and f..2f-1 the up projection; down: E matrices of d x f.
+ *   Y [B][d] float; ids [B][top_k] int32 and weights [B][top_k] float: the chosen experts by
+ *     falling logit and their p, each may be NULL.  All device.
+ * Logits are summed in FP64; products as in nq_w4_matmul; the activated rows are FP32.  One
+ * token's result does not depend on the others of the call beyond the order of summation
+ * over its experts, which is fixed (ascending).  Sizes: 1 <= d, f <= 65536,
+ * 1 <= top_k <= min(E, NQ_MOE_MAX_TOP_K), E <= NQ_MOE_MAX_EXPERTS, E 2f and E d <= 2^24
+ * (NQ_ERR_INVALID_ARG otherwise).  Enqueue only.
+ */
+nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void *router, int32_t E,
+                    int32_t top_k, int32_t renormalise, const uint32_t *gate_up,
+                    const void *gate_up_scales, const uint8_t *gate_up_zeros, const uint32_t *down,
+                    const void *down_scales, const uint8_t *down_zeros, int64_t f, int32_t group,
+                    float *Y, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
+                    nq_stream_t stream);
+
+/* ------------------------------------------------------------------------- */
 /* Step-level interface over the ADMM state held in the workspace.             */
 /* nq_lbadmm is nq_lbadmm_prepare + nq_lbadmm_iterate + nq_lbadmm_finish.      */
 /* The state fields can be read and written (checkpoint / resume, tests).      */
@@ -420,7 +513,9 @@ typedef enum {
     NQ_K_REFIT = 13,    /* least-squares scale refit                                 */
     NQ_K_NEWTON = 14,   /* tcgen05 Newton-Schulz update of G^-1                      */
     NQ_K_GD = 15,       /* gradient-descent latent update (solver variant)           */
-    NQ_K_COUNT = 16
+    NQ_K_W4 = 16,       /* 4-bit layers: quantiser, read-back, matrix product        */
+    NQ_K_MOE = 17,      /* expert layer on 4-bit experts                             */
+    NQ_K_COUNT = 18
 } nq_kernel_class;
 
 /* Number of kernel launches the library has issued in this process. */

@@ -22,7 +22,7 @@ from ._lib import (FIELDS, NQ_BF16, NQ_F32, NQ_PREC_BF16, NQ_PREC_FP32, NQError,
 __all__ = [
     "nq_bpw", "nq_rank_for_bpw", "nq_calib_stats", "nq_calib_precond", "nq_lbadmm",
     "nq_recon_error", "nq_pack_signs", "nq_binary_matmul", "nq_ls_refit", "LBState", "NQError",
-    "status_string", "lib",
+    "status_string", "lib", "nq_w4_quantize", "nq_w4_dequantize", "nq_w4_matmul", "nq_moe_w4",
     "nq_launch_count", "nq_profile_enable", "nq_profile_get", "nq_selftest",
     "nq_set_inverse_mode", "nq_set_tuning", "nq_set_latent_solver",
 ]
@@ -170,6 +170,141 @@ def nq_pack_signs(X):
     bits = torch.empty(rows, (r + 31) // 32, dtype=torch.int32, device=X.device)
     check("nq_pack_signs", lib.nq_pack_signs(_ptr(X), rows, r, _ptr(bits), _stream()))
     return bits
+
+
+def _w4_call(fn, dev, *args):
+    """Call a library function on the current stream of device ``dev``."""
+    if dev == torch.cuda.current_device():
+        code = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if code != _lib.NQ_OK:
+        raise NQError(fn, code)
+
+
+def _w4_layer(what, packed, scales, zeros, rows, n, group, dev):
+    """Check one packed array: ``rows`` rows (its leading dimensions) of ``n`` columns."""
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    ld, ng = (n + 31) // 32 * 4, (n + group - 1) // group
+    for t, dt, width, name in ((packed, torch.int32, ld, ""), (scales, torch.bfloat16, ng, " scales"),
+                               (zeros, torch.uint8, ng, " zeros")):
+        if t is None and name == " zeros":
+            continue
+        if t.dtype != dt:
+            raise TypeError(f"{what}{name} must be {dt}, got {t.dtype}")
+        if tuple(t.shape) != (*rows, width):
+            raise ValueError(f"{what}{name} must have shape {(*rows, width)}, got {tuple(t.shape)}")
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError(f"{what}{name} must be contiguous and on the device of the input")
+
+
+def _w4_input(x, name, dims):
+    if not (x.is_cuda and x.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if x.dim() not in dims:
+        raise ValueError(f"{name} has {x.dim()} dimensions")
+    if x.numel() == 0:
+        raise ValueError(f"{name} is empty")
+    return x.get_device(), _dtype(x)
+
+
+def _w4_ws(ws, need, dev):
+    if need == 0:
+        return None, 0
+    if ws is None:
+        ws = workspace(need, dev)
+    elif ws.get_device() != dev or not ws.is_contiguous() or ws.element_size() != 1:
+        raise ValueError("ws must be a contiguous byte tensor on the device of the input")
+    return ws.data_ptr(), ws.numel()
+
+
+def nq_w4_quantize(W, group=128, d_in=None, symmetric=True, grid=1):
+    """4-bit codes of W (m x n) with one scale per ``group`` columns of a row.
+
+    ``d_in`` (n) weights the error of the clipping search over ``grid`` candidates.  Returns
+    dict(packed, scales, zeros): int32 (m, 4 ceil(n / 32)), bfloat16 and uint8 (m, ceil(n /
+    group)); zeros is None when ``symmetric``.
+    """
+    dev, dt = _w4_input(W, "W", (2,))
+    m, n = W.shape
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    if d_in is not None and not (d_in.get_device() == dev and d_in.dtype == torch.float32 and
+                                 d_in.is_contiguous() and tuple(d_in.shape) == (n,)):
+        raise ValueError("d_in must be a contiguous float32 vector of length n on W's device")
+    ng = (n + group - 1) // group
+    packed = torch.empty(m, (n + 31) // 32 * 4, dtype=torch.int32, device=W.device)
+    scales = torch.empty(m, ng, dtype=torch.bfloat16, device=W.device)
+    zeros = None if symmetric else torch.empty(m, ng, dtype=torch.uint8, device=W.device)
+    _w4_call("nq_w4_quantize", dev, W.data_ptr(), dt, m, n,
+             None if d_in is None else d_in.data_ptr(), group, grid, packed.data_ptr(),
+             scales.data_ptr(), None if zeros is None else zeros.data_ptr())
+    return dict(packed=packed, scales=scales, zeros=zeros)
+
+
+def nq_w4_dequantize(packed, scales, n, group=128, zeros=None, dtype=torch.float32):
+    """The m x n matrix that 4-bit codes stand for (float32 exact, bfloat16 rounded)."""
+    if not packed.is_cuda or packed.dim() != 2 or packed.numel() == 0 or n < 1:
+        raise ValueError("packed must be a non-empty two-dimensional CUDA tensor and n positive")
+    dev, m = packed.get_device(), packed.shape[0]
+    _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
+    W = torch.empty(m, n, dtype=dtype, device=packed.device)
+    _w4_call("nq_w4_dequantize", dev, packed.data_ptr(), scales.data_ptr(),
+             None if zeros is None else zeros.data_ptr(), m, n, group, W.data_ptr(), _dtype(W))
+    return W
+
+
+def nq_w4_matmul(packed, scales, X, group=128, zeros=None, ws=None):
+    """Y = X W^T for a 4-bit layer and X of shape (B, n) or (n,); returns float32 Y."""
+    dev, dt = _w4_input(X, "X", (1, 2))
+    n = X.shape[-1]
+    B = X.shape[0] if X.dim() == 2 else 1
+    m = packed.shape[0]
+    _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
+    Y = torch.empty((B, m) if X.dim() == 2 else (m,), dtype=torch.float32, device=X.device)
+    ws_ptr, ws_bytes = _w4_ws(ws, lib.nq_w4_workspace_size(m, n, dt, B), dev)
+    _w4_call("nq_w4_matmul", dev, packed.data_ptr(), scales.data_ptr(),
+             None if zeros is None else zeros.data_ptr(), m, n, group, X.data_ptr(), dt, B,
+             Y.data_ptr(), ws_ptr, ws_bytes)
+    return Y
+
+
+def nq_moe_w4(X, router, gate_up, gate_up_scales, down, down_scales, top_k, group=128,
+              gate_up_zeros=None, down_zeros=None, renormalise=True, ws=None, want_routing=False):
+    """Mixture-of-experts layer with 4-bit experts for a few tokens X (B, d).
+
+    router (E, d) of X's dtype; gate_up packed (E, 2f, .) with the gate rows first; down packed
+    (E, d, .) over f columns.  Returns float32 Y (B, d), or (Y, ids, weights) with the chosen
+    experts (B, top_k) by falling logit and their weights.
+    """
+    dev, dt = _w4_input(X, "X", (2,))
+    B, d = X.shape
+    if gate_up.dim() != 3 or gate_up.shape[1] % 2 or gate_up.numel() == 0:
+        raise ValueError("gate_up must have shape (E, 2f, words)")
+    E, f = gate_up.shape[0], gate_up.shape[1] // 2
+    if router.get_device() != dev or router.dtype != X.dtype or not router.is_contiguous() or \
+            tuple(router.shape) != (E, d):
+        raise ValueError(f"router must be a contiguous {X.dtype} tensor of shape {(E, d)} on X's device")
+    _w4_layer("gate_up", gate_up, gate_up_scales, gate_up_zeros, (E, 2 * f), d, group, dev)
+    _w4_layer("down", down, down_scales, down_zeros, (E, d), f, group, dev)
+    Y = torch.empty(B, d, dtype=torch.float32, device=X.device)
+    ids = weights = None
+    if want_routing:
+        ids = torch.empty(B, top_k, dtype=torch.int32, device=X.device)
+        weights = torch.empty(B, top_k, dtype=torch.float32, device=X.device)
+    need = lib.nq_moe_workspace_size(B, d, f, E, top_k, dt)
+    if need == 0:
+        raise NQError("nq_moe_workspace_size", _lib.NQ_ERR_INVALID_ARG)
+    ws_ptr, ws_bytes = _w4_ws(ws, need, dev)
+    _w4_call("nq_moe_w4", dev, X.data_ptr(), dt, B, d, router.data_ptr(), E, top_k,
+             1 if renormalise else 0, gate_up.data_ptr(), gate_up_scales.data_ptr(),
+             None if gate_up_zeros is None else gate_up_zeros.data_ptr(), down.data_ptr(),
+             down_scales.data_ptr(), None if down_zeros is None else down_zeros.data_ptr(), f,
+             group, Y.data_ptr(), None if ids is None else ids.data_ptr(),
+             None if weights is None else weights.data_ptr(), ws_ptr, ws_bytes)
+    return (Y, ids, weights) if want_routing else Y
 
 
 def nq_set_inverse_mode(mode):

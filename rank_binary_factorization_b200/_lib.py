@@ -59,6 +59,15 @@ SIGNATURES = {
                             c_i32, c_vp, c_vp, c_sz, c_vp]),
     "nq_binary_matmul": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64,
                                  c_vp, c_vp, c_sz, c_vp]),
+    "nq_w4_quantize": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp,
+                               c_vp]),
+    "nq_w4_dequantize": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i32, c_vp]),
+    "nq_w4_workspace_size": (c_sz, [c_i64, c_i64, c_i32, c_i64]),
+    "nq_w4_matmul": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i32, c_vp, c_i32, c_i64, c_vp, c_vp,
+                             c_sz, c_vp]),
+    "nq_moe_workspace_size": (c_sz, [c_i64, c_i64, c_i64, c_i32, c_i32, c_i32]),
+    "nq_moe_w4": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
+                          c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "nq_lbadmm_prepare": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_i32, c_u64, c_i32,
                                   c_vp, c_vp, c_sz, c_vp]),
     "nq_lbadmm_iterate": (c_i32, [c_i64, c_i64, c_i32, c_f32, c_f32, c_i32, c_i32, c_i32, c_vp,
@@ -80,7 +89,8 @@ SIGNATURES = {
 }
 NQ_SELFTEST_WAIT_TIMEOUT, NQ_SELFTEST_NOT_SPD = 0, 1
 KERNEL_CLASSES = ["calib", "calib_finalize", "prep", "gram", "chol", "rhs", "solve", "svid",
-                  "objective", "finish", "recon", "ginv", "binary", "refit", "newton", "gd"]
+                  "objective", "finish", "recon", "ginv", "binary", "refit", "newton", "gd", "w4",
+                  "moe"]
 
 for _name, (_res, _args) in SIGNATURES.items():
     _f = getattr(lib, _name)

@@ -14,6 +14,7 @@
 #include "gemm_tc.cuh"
 #include "kernels.cuh"
 #include "layout.h"
+#include "w4.cuh"
 
 using namespace nq;
 
@@ -74,7 +75,7 @@ bool g_prof_on = false;
 const char *const kClassNames[NQ_K_COUNT] = {
     "nq.calib", "nq.calib_finalize", "nq.prep", "nq.gram", "nq.chol", "nq.rhs",
     "nq.solve", "nq.svid", "nq.objective", "nq.finish", "nq.recon", "nq.ginv", "nq.binary",
-    "nq.refit", "nq.newton", "nq.gd"};
+    "nq.refit", "nq.newton", "nq.gd", "nq.w4", "nq.moe"};
 
 // Scope of one kernel class's launches: an NVTX range on the host timeline (seen by
 // profilers; inert otherwise) and, when recording is on, a CUDA event pair on the stream.
@@ -1374,6 +1375,133 @@ nq_status nq_binary_matmul(const uint32_t *U_packed, const uint32_t *V_packed, c
         ep.s1 = s1;
         NQ_CK(tc::launch_gemm(maps, ep, tc::EPI_SCALE, BN, s));
     }
+    return NQ_OK;
+}
+
+// ---- 4-bit layers -------------------------------------------------------------------------
+static bool w4_args_ok(const void *packed, const void *scales, int64_t m, int64_t n, int32_t group) {
+    return packed && scales && aligned(packed, 16) && aligned(scales, 2) && m >= 1 && n >= 1 &&
+           m <= w4::kMaxRows && n <= kMaxDim && (group == 32 || group == 64 || group == 128);
+}
+static inline bool dtype_ok(int dt) { return dt == NQ_F32 || dt == NQ_BF16; }
+static inline bool typed(const void *p, int dt) { return p && aligned(p, dt == NQ_BF16 ? 2 : 4); }
+
+static w4::Mat w4_mat(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t n,
+                      int32_t group) {
+    return {packed, static_cast<const __nv_bfloat16 *>(scales), zeros, (int)n,
+            (int)w4::row_words(n), (int)w4::row_groups(n, group)};
+}
+
+nq_status nq_w4_quantize(const void *W, nq_dtype dt, int64_t m, int64_t n, const float *d_in,
+                         int32_t group, int32_t grid, uint32_t *packed, void *scales,
+                         uint8_t *zeros, nq_stream_t stream) {
+    if (!dtype_ok(dt) || !typed(W, dt) || !w4_args_ok(packed, scales, m, n, group) || grid < 1 ||
+        grid > NQ_W4_MAX_GRID || (d_in && !aligned(d_in, 4)))
+        return NQ_ERR_INVALID_ARG;
+    if (nq_status st = check_device()) return st;
+    ProfScope ps(NQ_K_W4, cs(stream));
+    NQ_CK(w4::quantize(W, dt == NQ_BF16, m, n, d_in, group, grid, packed,
+                       static_cast<__nv_bfloat16 *>(scales), zeros, cs(stream)));
+    return NQ_OK;
+}
+
+nq_status nq_w4_dequantize(const uint32_t *packed, const void *scales, const uint8_t *zeros,
+                           int64_t m, int64_t n, int32_t group, void *W, nq_dtype dt,
+                           nq_stream_t stream) {
+    if (!dtype_ok(dt) || !typed(W, dt) || !w4_args_ok(packed, scales, m, n, group))
+        return NQ_ERR_INVALID_ARG;
+    if (nq_status st = check_device()) return st;
+    ProfScope ps(NQ_K_W4, cs(stream));
+    NQ_CK(w4::dequantize(w4_mat(packed, scales, zeros, n, group), m, group, W, dt == NQ_BF16,
+                         cs(stream)));
+    return NQ_OK;
+}
+
+size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B) {
+    if (m < 1 || n < 1 || B < 1 || m > w4::kMaxRows || n > kMaxDim || B > kMaxDim || dt != NQ_F32)
+        return 0;
+    return align_up((size_t)B * w4::kTerms * w4::split_ld(n) * 2);
+}
+
+nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,
+                       int64_t n, int32_t group, const void *X, nq_dtype dt, int64_t B, float *Y,
+                       void *ws, size_t ws_bytes, nq_stream_t stream) {
+    if (!dtype_ok(dt) || !typed(X, dt) || !Y || !aligned(Y, 4) ||
+        !w4_args_ok(packed, scales, m, n, group) || B < 1 || B > kMaxDim)
+        return NQ_ERR_INVALID_ARG;
+    nq_status st;
+    const size_t need = nq_w4_workspace_size(m, n, dt, B);
+    if (need && (st = check_ws(ws, ws_bytes, need))) return st;
+    if ((st = check_device())) return st;
+    ProfScope ps(NQ_K_W4, cs(stream));
+    NQ_CK(w4::matmul(w4_mat(packed, scales, zeros, n, group), m, group, X, dt == NQ_BF16, B, Y,
+                     at<__nv_bfloat16>(ws, 0), cs(stream)));
+    return NQ_OK;
+}
+
+namespace {
+struct MoeLayout {
+    size_t ids = 0, weights = 0, xt = 0, h = 0, total = 0;
+    MoeLayout(int64_t B, int64_t d, int64_t f, int top_k, int dt) {
+        size_t off = 0;
+        auto take = [&](size_t bytes) {
+            const size_t o = off;
+            off = align_up(off + bytes);
+            return o;
+        };
+        ids = take((size_t)B * top_k * 4);
+        weights = take((size_t)B * top_k * 4);
+        xt = take(dt == NQ_F32 ? (size_t)B * w4::kTerms * w4::split_ld(d) * 2 : 0);
+        h = take((size_t)B * top_k * w4::kTerms * w4::split_ld(f) * 2);
+        total = off;
+    }
+};
+
+bool moe_sizes_ok(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k) {
+    return B >= 1 && B <= NQ_MOE_MAX_TOKENS && d >= 1 && d <= kMaxDim && f >= 1 && f <= kMaxDim &&
+           E >= 1 && E <= NQ_MOE_MAX_EXPERTS && top_k >= 1 && top_k <= NQ_MOE_MAX_TOP_K &&
+           top_k <= E && 2 * E * f <= w4::kMaxRows && E * d <= w4::kMaxRows;
+}
+}  // namespace
+
+size_t nq_moe_workspace_size(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k,
+                             nq_dtype dt) {
+    if (!moe_sizes_ok(B, d, f, E, top_k) || !dtype_ok(dt)) return 0;
+    return MoeLayout(B, d, f, top_k, dt).total;
+}
+
+nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void *router, int32_t E,
+                    int32_t top_k, int32_t renormalise, const uint32_t *gate_up,
+                    const void *gate_up_scales, const uint8_t *gate_up_zeros, const uint32_t *down,
+                    const void *down_scales, const uint8_t *down_zeros, int64_t f, int32_t group,
+                    float *Y, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
+                    nq_stream_t stream) {
+    if (!dtype_ok(dt) || !typed(X, dt) || !typed(router, dt) || !moe_sizes_ok(B, d, f, E, top_k) ||
+        !w4_args_ok(gate_up, gate_up_scales, 2 * E * f, d, group) ||
+        !w4_args_ok(down, down_scales, E * d, f, group) || !Y || !aligned(Y, 4) ||
+        (ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4)) || renormalise < 0 ||
+        renormalise > 1)
+        return NQ_ERR_INVALID_ARG;
+    const MoeLayout L(B, d, f, top_k, dt);
+    nq_status st = check_ws(ws, ws_bytes, L.total);
+    if (st) return st;
+    if ((st = check_device())) return st;
+    w4::MoeArgs a;
+    a.X = X;
+    a.x_bf16 = dt == NQ_BF16;
+    a.B = (int)B, a.d = (int)d, a.f = (int)f, a.E = E, a.top_k = top_k;
+    a.renormalise = renormalise;
+    a.router = router;
+    a.gate_up = w4_mat(gate_up, gate_up_scales, gate_up_zeros, d, group);
+    a.down = w4_mat(down, down_scales, down_zeros, f, group);
+    a.group = group;
+    a.Y = Y;
+    a.ids = ids ? ids : at<int32_t>(ws, L.ids);
+    a.weights = weights ? weights : at<float>(ws, L.weights);
+    a.xt = at<__nv_bfloat16>(ws, L.xt);
+    a.h = at<__nv_bfloat16>(ws, L.h);
+    ProfScope ps(NQ_K_MOE, cs(stream));
+    NQ_CK(w4::moe(a, cs(stream)));
     return NQ_OK;
 }
 
