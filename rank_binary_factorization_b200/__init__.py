@@ -211,9 +211,9 @@ def _w4_input(x, name, dims):
 
 
 def _w4_ws(ws, need, dev):
-    if need == 0:
-        return None, 0
     if ws is None:
+        if need == 0:
+            return None, 0
         ws = workspace(need, dev)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.element_size() != 1:
         raise ValueError("ws must be a contiguous byte tensor on the device of the input")

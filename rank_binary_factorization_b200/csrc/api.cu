@@ -1418,9 +1418,9 @@ nq_status nq_w4_dequantize(const uint32_t *packed, const void *scales, const uin
 }
 
 size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B) {
-    if (m < 1 || n < 1 || B < 1 || m > w4::kMaxRows || n > kMaxDim || B > kMaxDim || dt != NQ_F32)
+    if (m < 1 || n < 1 || B < 1 || m > w4::kMaxRows || n > kMaxDim || B > kMaxDim || !dtype_ok(dt))
         return 0;
-    return align_up((size_t)B * w4::kTerms * w4::split_ld(n) * 2);
+    return align_up(w4::x_workspace(n, dt == NQ_BF16, B));
 }
 
 nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,
@@ -1441,7 +1441,7 @@ nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t
 
 namespace {
 struct MoeLayout {
-    size_t ids = 0, weights = 0, xt = 0, h = 0, total = 0;
+    size_t ids = 0, weights = 0, xw = 0, h = 0, total = 0;
     MoeLayout(int64_t B, int64_t d, int64_t f, int top_k, int dt) {
         size_t off = 0;
         auto take = [&](size_t bytes) {
@@ -1451,8 +1451,8 @@ struct MoeLayout {
         };
         ids = take((size_t)B * top_k * 4);
         weights = take((size_t)B * top_k * 4);
-        xt = take(dt == NQ_F32 ? (size_t)B * w4::kTerms * w4::split_ld(d) * 2 : 0);
-        h = take((size_t)B * top_k * w4::kTerms * w4::split_ld(f) * 2);
+        xw = take((size_t)B * (dt == NQ_BF16 ? 1 : w4::kTerms) * w4::padded(d) * 2);
+        h = take((size_t)B * top_k * w4::kTerms * w4::padded(f) * 2);
         total = off;
     }
 };
@@ -1498,7 +1498,7 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     a.Y = Y;
     a.ids = ids ? ids : at<int32_t>(ws, L.ids);
     a.weights = weights ? weights : at<float>(ws, L.weights);
-    a.xt = at<__nv_bfloat16>(ws, L.xt);
+    a.xw = at<__nv_bfloat16>(ws, L.xw);
     a.h = at<__nv_bfloat16>(ws, L.h);
     ProfScope ps(NQ_K_MOE, cs(stream));
     NQ_CK(w4::moe(a, cs(stream)));

@@ -26,13 +26,16 @@ __global__ void __launch_bounds__(32 * kMoeWarps) moe_router_kernel(const MoeArg
         v = warp_sum(v);
         if (lane == 0) logit[e] = v;
     }
-    if constexpr (sizeof(T) == 4) {
-        const int ldx = (int)round_up(a.d, 8);
-        for (int k = threadIdx.x; k < ldx; k += blockDim.x) {
-            __nv_bfloat16 t[kTerms];
-            split_terms(k < a.d ? (float)x[k] : 0.f, t);
+    const int words = (int)(padded(a.d) / 8);
+    for (int wd = threadIdx.x; wd < words; wd += blockDim.x) {
+        uint4 *dst = reinterpret_cast<uint4 *>(a.xw);
+        if constexpr (sizeof(T) == 2) {
+            dst[(int64_t)b * words + wd] = x_word(x, wd * 8, a.d);
+        } else {
+            uint4 w[kTerms];
+            x_words(x, wd * 8, a.d, w);
 #pragma unroll
-            for (int i = 0; i < kTerms; ++i) a.xt[((int64_t)b * kTerms + i) * ldx + k] = t[i];
+            for (int t = 0; t < kTerms; ++t) dst[((int64_t)b * kTerms + t) * words + wd] = w[t];
         }
     }
     __syncthreads();
@@ -123,140 +126,183 @@ __device__ void build_lists(Lists &L, const int32_t *ids, int npairs, int E) {
 }
 
 // ---- gate and up projections, activation ----------------------------------------------
-// CTA: 16 of an expert's f rows, gate and up side by side (two row tiles of a warp), for the
-// expert's pairs, 8 columns at a time.  h leaves in kTerms BF16 columns.
-template <int VW>
-__global__ void __launch_bounds__(32 * kMoeWarps) moe_gate_up_kernel(const MoeArgs a) {
-    __shared__ Lists L;
-    __shared__ float red[kMoeWarps][32][9];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    build_lists(L, a.ids, a.B * a.top_k, a.E);
-    if ((int)blockIdx.y >= L.active) return;
-    const int e = L.expert[blockIdx.y];
-    const int r0 = blockIdx.x * 16;
-    int64_t row[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            row[i][h] = ((int64_t)e * 2 + i) * a.f + min(r0 + 8 * h + (lane >> 2), a.f - 1);
-    const int terms = a.x_bf16 ? 1 : kTerms;
-    const int64_t ldx = a.x_bf16 ? a.d : split_ld(a.d);
-    const __nv_bfloat16 *x = a.x_bf16 ? static_cast<const __nv_bfloat16 *>(a.X) : a.xt;
-    Mat M = a.gate_up;
-    const bool xvec = !a.x_bf16 || (a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0);
-    if (xvec) M.n = (int)split_ld(a.d);
-    const int64_t ldh = split_ld(a.f);
-    const int per = 8 / terms;
-    const int p1 = L.first[blockIdx.y + 1];
-    for (int p0 = L.first[blockIdx.y]; p0 < p1; p0 += per) {
-        const int np = min(per, p1 - p0);
-        const int c = lane >> 2;
-        const __nv_bfloat16 *col[1] = {nullptr};
-        if (c < np * terms)
-            col[0] = x + ((int64_t)(L.pairs[p0 + c / terms] / a.top_k) * terms + c % terms) * ldx;
-        float acc[2][1][4] = {};
-        group_products<VW, 2, 1>(acc, M, row, col, xvec, warp, kMoeWarps);
+// Job: 16 of an expert's f rows, gate and up side by side (two row tiles), against up to 8
+// columns of its pairs.  h leaves in kTerms BF16 columns.  A CTA does one expert's jobs.
+struct GateUpProb {
+    int jobs, WK;
+    static constexpr uint32_t half_stride = 0;
+    const MoeArgs &a;
+    const Lists &L;
+    Red<2, 1> *red;
+    int terms, per, e, first, pairs, r0, p0 = 0, np = 0;
+    int64_t ldx, ldh;
+
+    __device__ __forceinline__ int first_row(int, int wr, int i) const {
+        return (e * 2 + i) * a.f + r0 + wr * 16;
+    }
+    __device__ __forceinline__ int last_row(int, int i) const { return (e * 2 + i + 1) * a.f - 1; }
+    __device__ __forceinline__ void ready() const {}
+    __device__ __forceinline__ void begin(int job) {
+        p0 = first + job * per;
+        np = min(per, first + pairs - p0);
+    }
+    __device__ __forceinline__ const char *col(int) const {
+        const int c = min(((int)threadIdx.x & 31) >> 2, np * terms - 1);
+        return reinterpret_cast<const char *>(
+            a.xw + ((int64_t)(L.pairs[p0 + c / terms] / a.top_k) * terms + c % terms) * ldx);
+    }
+    __device__ __forceinline__ void end(int job, const float (&acc)[2][1][4]) {
+        Red<2, 1> &R = red[job & 1];
+        R.put(acc);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                red[warp][16 * i + 8 * (q >> 1) + (lane >> 2)][2 * (lane & 3) + (q & 1)] =
-                    acc[i][0][q];
-        __syncthreads();
-        for (int o = threadIdx.x; o < 16 * np; o += blockDim.x) {
-            const int r = o % 16, p = o / 16;
-            if (r0 + r >= ldh) continue;
-            float g = 0.f, u = 0.f;
-            for (int t = terms - 1; t >= 0; --t)
-#pragma unroll
-                for (int w = 0; w < kMoeWarps; ++w) {
-                    g += red[w][r][p * terms + t];
-                    u += red[w][16 + r][p * terms + t];
-                }
+        const int rows = 16 * (kWarps / WK);
+        for (int o = threadIdx.x; o < rows * np; o += 32 * kWarps) {
+            const int r = o % rows, p = o / rows, k = r0 + r;
+            if (k >= ldh) continue;
+            const float g = R.sum(r / 16, WK, r % 16, p * terms, terms),
+                        u = R.sum(r / 16, WK, 16 + r % 16, p * terms, terms);
             __nv_bfloat16 ht[kTerms];
-            split_terms(r0 + r < a.f ? g / (1.f + expf(-g)) * u : 0.f, ht);
+            split_terms(k < a.f ? g / (1.f + expf(-g)) * u : 0.f, ht);
 #pragma unroll
             for (int t = 0; t < kTerms; ++t)
-                a.h[((int64_t)L.pairs[p0 + p] * kTerms + t) * ldh + r0 + r] = ht[t];
+                a.h[((int64_t)L.pairs[p0 + p] * kTerms + t) * ldh + in_word(k)] = ht[t];
         }
     }
+};
+
+template <int VW, bool Z>
+__global__ void __launch_bounds__(32 * kWarps, 2) moe_gate_up_kernel(const MoeArgs a) {
+    extern __shared__ __align__(1024) char sm[];
+    Red<2, 1> *red = reinterpret_cast<Red<2, 1> *>(sm + ring_bytes<2>());
+    Lists &L = *reinterpret_cast<Lists *>(red + 2);
+    build_lists(L, a.ids, a.B * a.top_k, a.E);
+    if ((int)blockIdx.y >= L.active) return;
+    const int WK = k_ranges(a.d);
+    GateUpProb P{0, WK, a, L, red};
+    P.terms = a.x_bf16 ? 1 : kTerms;
+    P.per = 8 / P.terms;
+    P.e = L.expert[blockIdx.y];
+    P.first = L.first[blockIdx.y];
+    P.pairs = L.first[blockIdx.y + 1] - P.first;
+    P.r0 = blockIdx.x * 16 * (kWarps / WK);
+    P.jobs = (P.pairs + P.per - 1) / P.per;
+    P.ldx = padded(a.d);
+    P.ldh = padded(a.f);
+    run_products<VW, Z, false, 2, 1>(P, a.gate_up, a.svec_gate_up, WK, sm);
 }
 
 // ---- down projection and combination ---------------------------------------------------
-// CTA: 16 rows of d, all active experts in ascending order; y is summed in shared memory.
-template <int VW>
-__global__ void __launch_bounds__(32 * kMoeWarps) moe_down_kernel(const MoeArgs a) {
-    __shared__ Lists L;
-    __shared__ float red[kMoeWarps][16][9];
-    __shared__ float y[NQ_MOE_MAX_TOKENS][16];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    build_lists(L, a.ids, a.B * a.top_k, a.E);
-    for (int o = threadIdx.x; o < 16 * a.B; o += blockDim.x) y[o / 16][o % 16] = 0.f;
-    const int r0 = blockIdx.x * 16;
-    const int64_t ldh = split_ld(a.f);
-    Mat M = a.down;
-    M.n = (int)ldh;
-    constexpr int per = 8 / kTerms;
-    for (int i = 0; i < L.active; ++i) {
-        int64_t row[1][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            row[0][h] = (int64_t)L.expert[i] * a.d + min(r0 + 8 * h + (lane >> 2), a.d - 1);
-        const int p1 = L.first[i + 1];
-        for (int p0 = L.first[i]; p0 < p1; p0 += per) {
-            const int np = min(per, p1 - p0);
-            const int c = lane >> 2;
-            const __nv_bfloat16 *col[1] = {nullptr};
-            if (c < np * kTerms)
-                col[0] = a.h + ((int64_t)L.pairs[p0 + c / kTerms] * kTerms + c % kTerms) * ldh;
-            float acc[1][1][4] = {};
-            group_products<VW, 1, 1>(acc, M, row, col, true, warp, kMoeWarps);
-            __syncthreads();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                red[warp][8 * (q >> 1) + (lane >> 2)][2 * (lane & 3) + (q & 1)] = acc[0][0][q];
-            __syncthreads();
-            for (int o = threadIdx.x; o < 16 * np; o += blockDim.x) {
-                const int r = o % 16, p = o / 16, pair = L.pairs[p0 + p];
-                float v = 0.f;
-#pragma unroll
-                for (int t = kTerms - 1; t >= 0; --t)
-#pragma unroll
-                    for (int w = 0; w < kMoeWarps; ++w) v += red[w][r][p * kTerms + t];
-                y[pair / a.top_k][r] += a.weights[pair] * v;
-            }
+// CTA: one block of rows of d, all active experts in ascending order (jobs: chunks of an
+// expert's pairs); y is summed in shared memory.
+struct DownProb {
+    int jobs, WK;
+    static constexpr uint32_t half_stride = 0;
+    const MoeArgs &a;
+    const Lists &L;
+    Red<1, 1> *red;
+    float *y;                              // [B][rows]
+    const short *job_expert, *job_pair;    // active expert and first pair of a job
+    int r0;
+    int64_t ldh;
+    int p0 = 0, np = 0;
+
+    __device__ __forceinline__ int first_row(int job, int wr, int) const {
+        return L.expert[job_expert[job]] * a.d + r0 + wr * 16;
+    }
+    __device__ __forceinline__ int last_row(int job, int) const {
+        return (L.expert[job_expert[job]] + 1) * a.d - 1;
+    }
+    __device__ __forceinline__ void ready() const {}
+    __device__ __forceinline__ void begin(int job) {
+        p0 = job_pair[job];
+        np = min(8 / kTerms, L.first[job_expert[job] + 1] - p0);
+    }
+    __device__ __forceinline__ const char *col(int) const {
+        const int c = min(((int)threadIdx.x & 31) >> 2, np * kTerms - 1);
+        return reinterpret_cast<const char *>(
+            a.h + ((int64_t)L.pairs[p0 + c / kTerms] * kTerms + c % kTerms) * ldh);
+    }
+    __device__ __forceinline__ void end(int job, const float (&acc)[1][1][4]) {
+        Red<1, 1> &R = red[job & 1];
+        R.put(acc);
+        __syncthreads();
+        // one pair of a token per expert, and a barrier between two jobs: fixed order
+        const int rows = 16 * (kWarps / WK);
+        for (int o = threadIdx.x; o < rows * np; o += 32 * kWarps) {
+            const int r = o % rows, p = o / rows, pair = L.pairs[p0 + p];
+            y[pair / a.top_k * rows + r] +=
+                a.weights[pair] * R.sum(r / 16, WK, r % 16, p * kTerms, kTerms);
         }
     }
+};
+
+template <int VW, bool Z>
+__global__ void __launch_bounds__(32 * kWarps, 2) moe_down_kernel(const MoeArgs a) {
+    extern __shared__ __align__(1024) char sm[];
+    Red<1, 1> *red = reinterpret_cast<Red<1, 1> *>(sm + ring_bytes<1>());
+    Lists &L = *reinterpret_cast<Lists *>(red + 2);
+    short *job_expert = reinterpret_cast<short *>(&L + 1);
+    short *job_pair = job_expert + kMoeMaxPairs;
+    float *y = reinterpret_cast<float *>(job_pair + kMoeMaxPairs);
+    __shared__ int njobs;
+    const int WK = k_ranges(a.f), rows = 16 * (kWarps / WK);
+    build_lists(L, a.ids, a.B * a.top_k, a.E);
+    for (int o = threadIdx.x; o < rows * a.B; o += blockDim.x) y[o] = 0.f;
+    if (threadIdx.x == 0) {
+        int n = 0;
+        for (int i = 0; i < L.active; ++i)
+            for (int p = L.first[i]; p < L.first[i + 1]; p += 8 / kTerms, ++n)
+                job_expert[n] = (short)i, job_pair[n] = (short)p;
+        njobs = n;
+    }
     __syncthreads();
-    for (int o = threadIdx.x; o < 16 * a.B; o += blockDim.x)
-        if (r0 + o % 16 < a.d) a.Y[(int64_t)(o / 16) * a.d + r0 + o % 16] = y[o / 16][o % 16];
+    DownProb P{njobs, WK, a, L, red, y, job_expert, job_pair, (int)blockIdx.x * rows, padded(a.f)};
+    run_products<VW, Z, false, 1, 1>(P, a.down, a.svec_down, WK, sm);
+    __syncthreads();
+    for (int o = threadIdx.x; o < rows * a.B; o += blockDim.x)
+        if (P.r0 + o % rows < a.d) a.Y[(int64_t)(o / rows) * a.d + P.r0 + o % rows] = y[o];
+}
+
+template <class K>
+static cudaError_t moe_launch(K kern, dim3 grid, int smem, const MoeArgs &a, cudaStream_t st,
+                              std::atomic<uint64_t> &configured) {
+    cudaError_t e = ensure_smem_limit((const void *)kern, smem, configured);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, 32 * kWarps, smem, st>>>(a);
+    count_launch();
+    return cudaGetLastError();
 }
 
 template <int VW>
-static void moe_experts(const MoeArgs &a, cudaStream_t st) {
+static cudaError_t moe_experts(const MoeArgs &a, cudaStream_t st) {
+    static std::atomic<uint64_t> c0[2], c1[2];
     const int pairs = a.B * a.top_k;
-    moe_gate_up_kernel<VW><<<dim3((unsigned)ceil_div(a.f, 16), (unsigned)(pairs < a.E ? pairs : a.E)),
-                             32 * kMoeWarps, 0, st>>>(a);
-    count_launch();
-    moe_down_kernel<VW><<<(unsigned)ceil_div(a.d, 16), 32 * kMoeWarps, 0, st>>>(a);
-    count_launch();
+    constexpr int s0 = ring_bytes<2>() + 2 * sizeof(Red<2, 1>) + sizeof(Lists);
+    constexpr int s1 = ring_bytes<1>() + 2 * sizeof(Red<1, 1>) + sizeof(Lists) + 4 * kMoeMaxPairs +
+                       NQ_MOE_MAX_TOKENS * 16 * kWarps * 4;
+    const int zu = a.gate_up.z != nullptr, zd = a.down.z != nullptr;
+    const int ru = 16 * (kWarps / k_ranges(a.d)), rd = 16 * (kWarps / k_ranges(a.f));
+    // the columns of h past f are written by the blocks that cover them
+    cudaError_t e = moe_launch(zu ? moe_gate_up_kernel<VW, true> : moe_gate_up_kernel<VW, false>,
+                               dim3((unsigned)ceil_div(padded(a.f), ru),
+                                    (unsigned)(pairs < a.E ? pairs : a.E)),
+                               s0, a, st, c0[zu]);
+    if (e != cudaSuccess) return e;
+    return moe_launch(zd ? moe_down_kernel<VW, true> : moe_down_kernel<VW, false>,
+                      dim3((unsigned)ceil_div(a.d, rd)), s1, a, st, c1[zd]);
 }
 
-cudaError_t moe(const MoeArgs &a, cudaStream_t st) {
+cudaError_t moe(const MoeArgs &args, cudaStream_t st) {
+    MoeArgs a = args;
+    a.svec_gate_up = scales_vec(a.gate_up, a.group);
+    a.svec_down = scales_vec(a.down, a.group);
     if (a.x_bf16)
         moe_router_kernel<__nv_bfloat16><<<(unsigned)a.B, 32 * kMoeWarps, 0, st>>>(a);
     else
         moe_router_kernel<float><<<(unsigned)a.B, 32 * kMoeWarps, 0, st>>>(a);
     count_launch();
-    if (a.group == 32)
-        moe_experts<1>(a, st);
-    else if (a.group == 64)
-        moe_experts<2>(a, st);
-    else
-        moe_experts<4>(a, st);
-    return cudaGetLastError();
+    auto run = a.group == 32 ? moe_experts<1> : a.group == 64 ? moe_experts<2> : moe_experts<4>;
+    return run(a, st);
 }
 
 }  // namespace w4

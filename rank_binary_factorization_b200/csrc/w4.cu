@@ -217,108 +217,160 @@ cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf
 }
 
 // ---------------------------------------------------------------------------------
-// Matrix product for few columns: one CTA per 16 MT rows and chunk of NT x 8 columns, its
-// 8 warps interleaved over the groups of the k axis, joined in shared memory in a fixed
-// order.
+// Matrix product for few columns: persistent CTAs walk the row tiles (run_products).
 // ---------------------------------------------------------------------------------
-constexpr int kWarps = 8;
+template <int MT, int NT, bool XS>
+struct GemvProb {
+    int jobs, WK;
+    int terms, nb, cols;                   // columns per row of X; rows of X, columns of this CTA
+    int m, lrows;                          // rows of W; log2 of the rows of a job
+    int64_t b0;                            // its first row of X
+    const __nv_bfloat16 *xw;               // its columns (global memory), ldx apart
+    int64_t ldx;
+    uint32_t xs, half_stride;              // its columns (shared memory)
+    float *Y;
+    Red<MT, NT> *red;                      // two, used in turn: one barrier per job
 
-// FP32 X (B x n) into kTerms BF16 columns per row, zero padded to ldx.
+    // job k of a CTA is row block blockIdx.x + k gridDim.x of 16 MT (8 / WK) rows
+    __device__ __forceinline__ int block_row(int job) const {
+        return (int)(blockIdx.x + (unsigned)job * gridDim.x) << lrows;
+    }
+    __device__ __forceinline__ int first_row(int job, int wr, int i) const {
+        return block_row(job) + 16 * (MT * wr + i);
+    }
+    __device__ __forceinline__ int last_row(int, int) const { return m - 1; }
+    __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
+    __device__ __forceinline__ void begin(int) {}
+    __device__ __forceinline__ const char *col(int j) const {
+        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
+        if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));
+        return reinterpret_cast<const char *>(xw + c * ldx);
+    }
+    __device__ __forceinline__ void end(int job, const float (&acc)[MT][NT][4]) {
+        Red<MT, NT> &R = red[job & 1];
+        R.put(acc);
+        __syncthreads();
+        const int r0 = block_row(job);
+        for (int o = threadIdx.x; o < nb << lrows; o += 32 * kWarps) {
+            const int r = o & ((1 << lrows) - 1), b = o >> lrows;
+            if (r0 + r < m)
+                Y[(b0 + b) * m + r0 + r] = R.sum(r / (16 * MT), WK, r % (16 * MT), b * terms, terms);
+        }
+    }
+};
+
+// Whether the columns of a CTA are kept in shared memory: up to this many bytes of them leave
+// two CTAs an SM.
+constexpr int kXsBytes = 48 * 1024;
+
+template <int VW, bool Z, bool XS, int MT, int NT>
+__global__ void __launch_bounds__(32 * kWarps, 2)
+    gemv_kernel(const Mat M, int m, const void *X, int x_bf16, const __nv_bfloat16 *xw, int svec,
+                int WK, int64_t B, int blocks, float *__restrict__ Y) {
+    extern __shared__ __align__(1024) char sm[];
+    GemvProb<MT, NT, XS> P;
+    P.jobs = (int)((blocks - blockIdx.x + gridDim.x - 1) / gridDim.x);
+    P.WK = WK;
+    P.terms = x_bf16 ? 1 : kTerms;
+    const int per = 8 * NT / P.terms;
+    P.b0 = (int64_t)blockIdx.y * per;
+    P.nb = (int)min((int64_t)per, B - P.b0);
+    P.cols = P.nb * P.terms;
+    P.m = m, P.Y = Y;
+    P.lrows = 31 - __clz(16 * MT * (kWarps / WK));
+    P.ldx = padded(M.n);
+    P.xw = XS ? nullptr : xw + P.b0 * P.terms * P.ldx;
+    P.red = reinterpret_cast<Red<MT, NT> *>(sm + ring_bytes<MT>());
+    uint4 *xs = reinterpret_cast<uint4 *>(P.red + 2);
+    P.xs = (uint32_t)__cvta_generic_to_shared(xs);
+    P.half_stride = P.cols * 256;
+    if constexpr (XS) {
+        const int words = (int)(P.ldx / 8);
+        for (int o = threadIdx.x; o < words * P.nb; o += 32 * kWarps) {
+            const int b = o / words, wd = o % words;
+            const int64_t row = (P.b0 + b) * M.n;
+            if (x_bf16) {
+                xs[x_entry<VW>(wd / 16, wd % 16, b, P.cols)] =
+                    x_word(static_cast<const __nv_bfloat16 *>(X) + row, wd * 8, M.n);
+            } else {
+                uint4 w[kTerms];
+                x_words(static_cast<const float *>(X) + row, wd * 8, M.n, w);
+#pragma unroll
+                for (int t = 0; t < kTerms; ++t)
+                    xs[x_entry<VW>(wd / 16, wd % 16, b * kTerms + t, P.cols)] = w[t];
+            }
+        }
+    }
+    run_products<VW, Z, XS, MT, NT>(P, M, svec, WK, sm);
+}
+
+// X (B x n) as columns in word order: [B][1 or kTerms][padded(n)].
 __global__ void __launch_bounds__(256)
-    split_x_kernel(const float *__restrict__ X, int64_t B, int n, int ldx,
-                   __nv_bfloat16 *__restrict__ xt) {
+    x_words_kernel(const void *X, int x_bf16, int64_t B, int n, uint4 *__restrict__ xw) {
+    const int words = (int)(padded(n) / 8);
     const int64_t b = blockIdx.x;
-    const int k = blockIdx.y * blockDim.x + threadIdx.x;
-    if (k >= ldx) return;
-    __nv_bfloat16 t[kTerms];
-    split_terms(k < n ? X[b * n + k] : 0.f, t);
-#pragma unroll
-    for (int i = 0; i < kTerms; ++i) xt[(b * kTerms + i) * ldx + k] = t[i];
-}
-
-template <int VW, int MT, int NT>
-__global__ void __launch_bounds__(32 * kWarps)
-    gemv_kernel(const Mat M, int64_t m, const __nv_bfloat16 *__restrict__ x, int64_t ldx, int xvec,
-                int terms, int64_t B, float *__restrict__ Y) {
-    constexpr int R = 16 * MT, C = 8 * NT;
-    __shared__ float red[kWarps][R][C + 1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r0 = (int64_t)blockIdx.x * R;
-    const int per = C / terms;                       // rows of X in a chunk
-    const int64_t b0 = (int64_t)blockIdx.y * per;
-    const int nb = (int)min((int64_t)per, B - b0);
-    int64_t row[MT][2];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) row[i][h] = min(r0 + 16 * i + 8 * h + (lane >> 2), m - 1);
-    const __nv_bfloat16 *col[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int c = 8 * j + (lane >> 2);
-        col[j] = c < nb * terms ? x + (b0 * terms + c) * ldx : nullptr;
-    }
-    float acc[MT][NT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = 0.f;
-    group_products<VW, MT, NT>(acc, M, row, col, xvec, warp, kWarps);
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                red[warp][16 * i + 8 * (e >> 1) + (lane >> 2)][8 * j + 2 * (lane & 3) + (e & 1)] =
-                    acc[i][j][e];
-    __syncthreads();
-    for (int o = threadIdx.x; o < R * nb; o += 32 * kWarps) {
-        const int r = o % R, b = o / R;
-        if (r0 + r >= m) continue;
-        float v = 0.f;
-        for (int t = terms - 1; t >= 0; --t)
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += red[w][r][b * terms + t];
-        Y[(b0 + b) * m + r0 + r] = v;
-    }
-}
-
-template <int VW>
-static cudaError_t gemv(const Mat &M, int64_t m, const __nv_bfloat16 *x, int64_t ldx, int xvec,
-                        int terms, int64_t B, float *Y, cudaStream_t st) {
-    if (B * terms <= 8) {
-        const dim3 grid((unsigned)ceil_div(m, 16), (unsigned)ceil_div(B, 8 / terms));
-        gemv_kernel<VW, 1, 1><<<grid, 32 * kWarps, 0, st>>>(M, m, x, ldx, xvec, terms, B, Y);
+    const int wd = blockIdx.y * blockDim.x + threadIdx.x;
+    if (wd >= words) return;
+    if (x_bf16) {
+        xw[b * words + wd] = x_word(static_cast<const __nv_bfloat16 *>(X) + b * n, wd * 8, n);
     } else {
-        const dim3 grid((unsigned)ceil_div(m, 32), (unsigned)ceil_div(B, 16 / terms));
-        gemv_kernel<VW, 2, 2><<<grid, 32 * kWarps, 0, st>>>(M, m, x, ldx, xvec, terms, B, Y);
+        uint4 w[kTerms];
+        x_words(static_cast<const float *>(X) + b * n, wd * 8, n, w);
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) xw[(b * kTerms + t) * words + wd] = w[t];
     }
+}
+
+// Columns of X in the call, and whether a CTA keeps its own in shared memory.
+static bool x_shared(int64_t n, int x_bf16, int64_t B) {
+    const int64_t cols = B * (x_bf16 ? 1 : kTerms);
+    return cols <= 8 && cols * padded(n) * 2 <= kXsBytes;
+}
+
+size_t x_workspace(int64_t n, int x_bf16, int64_t B) {
+    if (x_shared(n, x_bf16, B)) return 0;
+    return (size_t)B * (x_bf16 ? 1 : kTerms) * padded(n) * 2;
+}
+
+template <int VW, bool Z, bool XS, int MT, int NT>
+static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
+                          int64_t B, float *Y, cudaStream_t st) {
+    const int terms = x_bf16 ? 1 : kTerms;
+    constexpr int fixed = ring_bytes<MT>() + 2 * sizeof(Red<MT, NT>);
+    const int smem = fixed + (XS ? (int)(B * terms * padded(M.n) * 2) : 0);
+    auto kern = gemv_kernel<VW, Z, XS, MT, NT>;
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = ensure_smem_limit((const void *)kern, fixed + (XS ? kXsBytes : 0), configured);
+    if (e != cudaSuccess) return e;
+    const int WK = k_ranges(M.n);
+    const int64_t blocks = ceil_div(m, 16 * MT * (kWarps / WK)), chunks = ceil_div(B, 8 * NT / terms);
+    int64_t ctas = 2 * (int64_t)device_sm_count() / chunks;
+    ctas = ctas < 1 ? 1 : ctas > blocks ? blocks : ctas;
+    kern<<<dim3((unsigned)ctas, (unsigned)chunks), 32 * kWarps, smem, st>>>(
+        M, (int)m, X, x_bf16, xw, scales_vec(M, 32 * VW), WK, B, (int)blocks, Y);
     count_launch();
     return cudaGetLastError();
 }
 
+template <int VW, bool Z>
+static cudaError_t gemv(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
+                        int64_t B, float *Y, cudaStream_t st) {
+    if (x_shared(M.n, x_bf16, B)) return gemv_t<VW, Z, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
+    if (B * (x_bf16 ? 1 : kTerms) <= 8)
+        return gemv_t<VW, Z, false, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
+    return gemv_t<VW, Z, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
+}
+
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
-                   float *Y, __nv_bfloat16 *xt, cudaStream_t st) {
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(X);
-    int64_t ldx = M.n;
-    int xvec = M.n % 8 == 0 && reinterpret_cast<uintptr_t>(X) % 16 == 0;
-    if (!x_bf16) {
-        ldx = split_ld(M.n);
-        split_x_kernel<<<dim3((unsigned)B, (unsigned)ceil_div(ldx, 256)), 256, 0, st>>>(
-            static_cast<const float *>(X), B, M.n, (int)ldx, xt);
+                   float *Y, __nv_bfloat16 *xw, cudaStream_t st) {
+    if (!x_shared(M.n, x_bf16, B)) {
+        x_words_kernel<<<dim3((unsigned)B, (unsigned)ceil_div(padded(M.n) / 8, 256)), 256, 0, st>>>(
+            X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw));
         count_launch();
-        x = xt;
-        xvec = 1;
     }
-    const int terms = x_bf16 ? 1 : kTerms;
-    Mat Mx = M;
-    if (xvec) Mx.n = (int)split_ld(M.n);     // the padding of a split column is zero
-    if (group == 32) return gemv<1>(Mx, m, x, ldx, xvec, terms, B, Y, st);
-    if (group == 64) return gemv<2>(Mx, m, x, ldx, xvec, terms, B, Y, st);
-    return gemv<4>(Mx, m, x, ldx, xvec, terms, B, Y, st);
+    auto run = M.z ? (group == 32 ? gemv<1, true> : group == 64 ? gemv<2, true> : gemv<4, true>)
+                   : (group == 32 ? gemv<1, false> : group == 64 ? gemv<2, false> : gemv<4, false>);
+    return run(M, m, X, x_bf16, xw, B, Y, st);
 }
 
 }  // namespace w4

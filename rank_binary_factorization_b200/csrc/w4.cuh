@@ -41,136 +41,67 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word as BF16 pair (q_i - z, q_{i+4} - z).  A code in the low bits
-// of the mantissa of 128.0 (ulp 1) is 128 + q; ``bias`` holds 128 + z twice.  Exact.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i, uint32_t bias) {
-    uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&bias));
-    return *reinterpret_cast<const uint32_t *>(&d);
+// Codes i and i + 4 of a word as the BF16 pair ((q_i - z) / 4, (q_{i+4} - z) / 4), exactly, for
+// i = 0, 1 (i = 2, 3: the word shifted right by 8).  Bits 0..3 of a half: the low mantissa
+// bits of 128.0 (ulp 1) make 128 + q.  Bits 4..7 of a half alone are the BF16 number
+// q 2^-129 for every q (subnormals and the first binade are one line), which 2^127 brings to
+// q / 4.  So four pairs cost one shift, four logical operations and four FMAs.
+struct ZeroPoint {
+    uint32_t lo, hi;      // -(128 + z) / 4 and -z / 4, twice each
+};
+// -32 has ulp 1/4: its low mantissa bits make -(32 + z / 4).
+__device__ __forceinline__ ZeroPoint zero_point(uint32_t z) {
+    const uint32_t lo = (0xc200u | z) * 0x10001u, c32 = 0x42004200u;
+    const __nv_bfloat162 hi = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&lo),
+                                      *reinterpret_cast<const __nv_bfloat162 *>(&c32));
+    return {lo, *reinterpret_cast<const uint32_t *>(&hi)};
+}
+__device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t code_pair0(uint32_t w, const ZeroPoint &z) {
+    return fma_pair((w & 0x000f000fu) | 0x43004300u, 0x3e803e80u /* 1/4 */, z.lo);
+}
+__device__ __forceinline__ uint32_t code_pair1(uint32_t w, const ZeroPoint &z) {
+    return fma_pair(w & 0x00f000f0u, 0x7f007f00u /* 2^127 */, z.hi);
+}
+constexpr float kCodeUnit = 4.f;   // the pairs hold codes in units of 1/4
+
+// 16 bytes global -> shared, asynchronously; zeros where ``in`` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(in ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint32_t zero_bias(uint32_t z) { return (0x4300u | (z & 15u)) * 0x10001u; }
+// ---- activations -----------------------------------------------------------------------
+// The product reads a column of activations as BF16 words of 8 values in the order of the
+// code pairs, (0,4) (1,5) (2,6) (3,7), zero from n up to a multiple of kUnit.
+constexpr int kUnit = 256;                       // columns of W in a unit of work
+constexpr int kHalf = 128;                       // a unit's halves: 4 words a lane
+NQ_HD int64_t padded(int64_t n) { return round_up(n, kUnit); }
 
-template <int VW>
-__device__ __forceinline__ void load_words(uint32_t (&w)[VW], const uint32_t *p) {
-    if constexpr (VW == 1) {
-        w[0] = __ldg(p);
-    } else if constexpr (VW == 2) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-        w[0] = v.x, w[1] = v.y;
-    } else {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    }
+__device__ __forceinline__ uint4 pair_order(const uint4 v) {
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                      __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
 }
 
-// Eight consecutive activations x[k .. k + 7] of one column, zero from n on.
-__device__ __forceinline__ uint4 load_x8(const __nv_bfloat16 *x, int k, int n, bool vec) {
-    if (vec) return k < n ? *reinterpret_cast<const uint4 *>(x + k) : make_uint4(0, 0, 0, 0);
+// Values x[k .. k + 7] of a BF16 vector of length n as a word; zero from n on.
+__device__ __forceinline__ uint4 x_word(const __nv_bfloat16 *x, int64_t k, int n) {
+    if (k + 8 <= n && (reinterpret_cast<uintptr_t>(x + k) & 15) == 0)
+        return pair_order(*reinterpret_cast<const uint4 *>(x + k));
     uint32_t h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         h[i] = k + i < n ? reinterpret_cast<const unsigned short *>(x)[k + i] : 0;
-    return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-}
-
-// acc[mt][nt] += W^ rows x columns over groups grp0, grp0 + step, ... < ng, for one warp.
-// The A fragment of an MMA is 16 rows of W (lane: rows lane/4 and lane/4 + 8), the B
-// fragment 8 columns (lane: column lane/4), so any order of the k axis serves as long as
-// both sides use it: lane%4 = t takes VW = g/32 consecutive words of a row, words
-// t VW .. t VW + VW - 1 of a group, so a group is 2 VW MMAs of exactly its own columns and
-// its sum is scaled once, in FP32.  Integers and BF16 activations multiply exactly.
-// row[mt][h]: row (lane/4 + 8h of tile mt) as a row index of M, clamped by the caller;
-// col[nt]: the lane's column of n-tile nt, or null for a column that is not there.
-template <int VW, int MT, int NT>
-__device__ __forceinline__ void group_products(float (&acc)[MT][NT][4], const Mat &M,
-                                               const int64_t (&row)[MT][2],
-                                               const __nv_bfloat16 *const (&col)[NT], bool xvec,
-                                               int grp0, int step) {
-    const int t = threadIdx.x & 3;
-    constexpr int U = VW == 4 ? 2 : 4;     // groups in flight per lane
-    for (int gr = grp0; gr < M.ng; gr += U * step) {
-        uint32_t w[U][MT][2][VW];
-        float s[U][MT][2];
-        uint32_t bias[U][MT][2];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int grp = gr + u * step;
-            const int word = (4 * grp + t) * VW;
-            const bool in = grp < M.ng && word < M.ld;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int v = 0; v < VW; ++v) w[u][i][h][v] = 0;
-                    if (in) load_words<VW>(w[u][i][h], M.q + row[i][h] * M.ld + word);
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int grp = gr + u * step;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    s[u][i][h] = 0.f;
-                    bias[u][i][h] = zero_bias(8);
-                    if (grp < M.ng) {
-                        const int64_t at = row[i][h] * M.ng + grp;
-                        s[u][i][h] = __bfloat162float(M.s[at]);
-                        if (M.z) bias[u][i][h] = zero_bias(__ldg(M.z + at));
-                    }
-                }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int grp = gr + u * step;
-            if (grp >= M.ng) break;
-            float c[MT][NT][4];
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[i][j][e] = 0.f;
-#pragma unroll
-            for (int v = 0; v < VW; ++v) {
-                const int k = ((4 * grp + t) * VW + v) * 8;
-                uint32_t b[NT][4];      // (x0,x4) (x1,x5) (x2,x6) (x3,x7): the code pairs' order
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint4 x = col[j] ? load_x8(col[j], k, M.n, xvec) : make_uint4(0, 0, 0, 0);
-                    b[j][0] = __byte_perm(x.x, x.z, 0x5410);
-                    b[j][1] = __byte_perm(x.x, x.z, 0x7632);
-                    b[j][2] = __byte_perm(x.y, x.w, 0x5410);
-                    b[j][3] = __byte_perm(x.y, x.w, 0x7632);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const uint32_t a[4] = {
-                            code_pair(w[u][i][0][v], 2 * p, bias[u][i][0]),
-                            code_pair(w[u][i][1][v], 2 * p, bias[u][i][1]),
-                            code_pair(w[u][i][0][v], 2 * p + 1, bias[u][i][0]),
-                            code_pair(w[u][i][1][v], 2 * p + 1, bias[u][i][1])};
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) mma16816(c[i][j], a, b[j][2 * p], b[j][2 * p + 1]);
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    acc[i][j][0] += s[u][i][0] * c[i][j][0];
-                    acc[i][j][1] += s[u][i][0] * c[i][j][1];
-                    acc[i][j][2] += s[u][i][1] * c[i][j][2];
-                    acc[i][j][3] += s[u][i][1] * c[i][j][3];
-                }
-        }
-    }
+    return make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
 }
 
 // The three BF16 terms of an FP32 value, each the leading 8 bits of what is left (rounded
@@ -183,6 +114,360 @@ __device__ __forceinline__ void split_terms(float x, __nv_bfloat16 (&t)[kTerms])
     t[2] = __float2bfloat16_rz(r1 - __bfloat162float(t[1]));
 }
 
+// The same of an FP32 vector: the words of its kTerms columns.
+__device__ __forceinline__ void x_words(const float *x, int64_t k, int n, uint4 (&w)[kTerms]) {
+    __nv_bfloat16 t[8][kTerms];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_terms(k + i < n ? x[k + i] : 0.f, t[i]);
+#pragma unroll
+    for (int j = 0; j < kTerms; ++j) {
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = __bfloat16_as_ushort(t[i][j]);
+        w[j] = make_uint4(h[0] | h[4] << 16, h[1] | h[5] << 16, h[2] | h[6] << 16, h[3] | h[7] << 16);
+    }
+}
+
+// Place of value k of a column in that order, within its word.
+NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
+
+// ---- rows x columns -----------------------------------------------------------------------
+// One CTA's products of packed rows with activation columns, job after job.
+//
+// A job is MT tiles of 16 rows, WR times over, against NT x 8 columns and the whole k axis.
+// The 8 warps are WR row groups of WK; the warps of a group split the k axis into contiguous
+// ranges of units and join in shared memory at the end of the job (WK = 8 where the axis has
+// units enough: the fewest rows a job, the most even spread of jobs over the SMs).  Every
+// warp runs its own ring of kStages asynchronous copies (one unit of its rows: 128 bytes of
+// codes a row) that carries on across jobs, so 16 MT kStages KB a CTA are on their way from
+// memory at any time and no warp waits for another within a job.  Scales and zero points of
+// a unit go to registers while the unit before it is worked on; the cursor that runs ahead
+// fetches a job's scales towards the SM when it enters the job.
+//
+// The A fragment of an MMA is 16 rows of W (lane: rows lane/4 and lane/4 + 8), the B
+// fragment 8 columns (lane: column lane/4), so any order of the k axis serves as long as
+// both sides use it: lane%4 = t takes VW = g/32 consecutive words of a row, words t VW ..
+// t VW + VW - 1 of a group, so a group is 2 VW MMAs of exactly its own columns, and its sum
+// is scaled once, in FP32.
+//
+// Shared memory of a unit: 128 bytes a row, its eight 16-byte chunks permuted with the row so
+// that the fragment loads (16, 8 or 4 bytes a lane for g = 128, 64, 32) meet every bank once.
+//
+// Columns past the last one repeat it: an MMA column reaches no other, and nobody reads its
+// sums.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
+//
+// Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
+// begin(job) (before the first activation of the job is read), col(j) -> the lane's column of
+// n-tile j of that job (XS: byte offset of its first word in shared memory, else address), and
+// end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
+constexpr int kWarps = 8;
+constexpr int kStages = 3;
+template <int MT>
+NQ_HD constexpr int ring_bytes() { return kWarps * kStages * MT * 2048; }
+// K-axis ranges of a row group for n columns.
+NQ_HD int k_ranges(int64_t n) {
+    const int64_t u = ceil_div(n, kUnit);
+    return u >= 8 ? 8 : u >= 4 ? 4 : u >= 2 ? 2 : 1;
+}
+
+// Word c (0..3) of lane t in a half: group c / VW, word c % VW of its VW.
+template <int VW>
+NQ_HD int lane_word(int t, int c) { return (c / VW) * 4 * VW + t * VW + c % VW; }
+
+// Shared-memory place (in 16-byte entries) of word wi of a half of column ``col`` of C: the
+// lanes of an MMA read 16 bytes each, 4 t side by side, two columns in two halves of the banks.
+template <int VW>
+__device__ __forceinline__ int x_entry(int half, int wi, int col, int C) {
+    const int c = VW == 4 ? wi & 3 : VW == 2 ? (wi >> 3) * 2 + (wi & 1) : wi >> 2;
+    const int t = VW == 4 ? wi >> 2 : VW == 2 ? (wi >> 1) & 3 : wi & 3;
+    return (half * C + col) * 16 + ((c ^ (col & 1)) << 2) + t;
+}
+
+// G scales (and zero points) of a row's unit, as registers; grp: the unit's first group.
+template <int G, bool Z>
+struct Scales {
+    static constexpr int NS = (G + 1) / 2, NZ = (G + 3) / 4;
+    uint32_t s[NS], z[NZ];
+    // vec: every row's unit starts on a multiple of G scales and ends inside the row
+    __device__ __forceinline__ void load(const Mat &M, int64_t at, int grp, bool vec) {
+        if (vec) {
+            const void *ps = M.s + at, *pz = M.z + at;
+            if constexpr (G == 2) {
+                s[0] = __ldg(static_cast<const uint32_t *>(ps));
+                if constexpr (Z) z[0] = __ldg(static_cast<const unsigned short *>(pz));
+            } else if constexpr (G == 4) {
+                const uint2 v = __ldg(static_cast<const uint2 *>(ps));
+                s[0] = v.x, s[1] = v.y;
+                if constexpr (Z) z[0] = __ldg(static_cast<const uint32_t *>(pz));
+            } else {
+                const uint4 v = __ldg(static_cast<const uint4 *>(ps));
+                s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
+                if constexpr (Z) {
+                    const uint2 u = __ldg(static_cast<const uint2 *>(pz));
+                    z[0] = u.x, z[1] = u.y;
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) s[i] = 0;
+#pragma unroll
+        for (int i = 0; i < NZ; ++i) z[i] = 0;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            if (grp + i < M.ng) {
+                s[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(M.s) + at + i)
+                            << (16 * (i & 1));
+                if constexpr (Z) z[i / 4] |= (uint32_t)(__ldg(M.z + at + i)) << (8 * (i & 3));
+            }
+    }
+    __device__ __forceinline__ float scale(int i) const {
+        return __uint_as_float(i & 1 ? s[i / 2] & 0xffff0000u : s[i / 2] << 16);
+    }
+    __device__ __forceinline__ ZeroPoint zero(int i) const {
+        if constexpr (Z) return zero_point(z[i / 4] >> (8 * (i & 3)) & 15u);
+        return zero_point(8);
+    }
+};
+// Whether Scales::load may take its vectors.
+inline bool scales_vec(const Mat &M, int group) {
+    const int G = kUnit / group;
+    return M.ng % G == 0 && reinterpret_cast<uintptr_t>(M.s) % (2 * G) == 0 &&
+           reinterpret_cast<uintptr_t>(M.z) % G == 0;
+}
+
+template <int VW, bool Z, bool XS, int MT, int NT, class Prob>
+__device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, int WK, char *ring) {
+    constexpr int G = kUnit / (32 * VW);         // groups of a unit
+    constexpr int kStage = MT * 2048;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int wr = warp / WK, wk = warp % WK;
+    const int units = (M.n + kUnit - 1) / kUnit;
+    const int u0 = units * wk / WK, u1 = units * (wk + 1) / WK;      // never empty
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(ring) + warp * kStages * kStage;
+    const int swz = VW == 4 ? (g & 1) << 2 : VW == 2 ? (g & 3) << 1 : g;
+
+    // Producer cursor: job pj, its units from pu on.  A lane copies chunk pc of rows pr, pr + 4,
+    // pr + 8, pr + 12 of a tile, each held to the last row that the tile may reach.
+    const int pr = lane >> 3, pc = lane & 7;
+    uint32_t put[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = pr + 4 * i;
+        const int sw = VW == 4 ? (r & 1) << 2 : VW == 2 ? (r & 3) << 1 : r & 7;
+        put[i] = r * 128 + ((pc ^ sw) << 4);
+    }
+    int pj = 0, pu = u0;
+    const uint32_t *src[MT][4];
+    auto enter = [&](int job) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int first = P.first_row(job, wr, m), last = P.last_row(job, m);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                src[m][i] = M.q + u0 * 32 + 4 * pc + (int64_t)min(first + pr + 4 * i, last) * M.ld;
+            // the job's scales: rows g and g + 8, 32 bytes a lane
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int grp = u0 * G + 16 * t;
+                if (grp < min(u1 * G, M.ng))
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                        M.s + grp + (int64_t)min(first + g + 8 * h, last) * M.ng));
+            }
+        }
+    };
+    auto issue = [&](uint32_t stage) {
+        if (pj < P.jobs) {
+            const bool in = pu * 32 + 4 * pc < M.ld;         // the row's words end here
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    copy16(stage + m * 2048 + put[i], src[m][i], in);
+                    src[m][i] += 32;
+                }
+            if (++pu == u1) {
+                pu = u0;
+                if (++pj < P.jobs) enter(pj);
+            }
+        }
+        copy_commit();
+    };
+
+    // Consumer: scales of a unit, activations of a half, one step ahead of their use.
+    int64_t at[MT][2];                           // the unit's first scale of rows g and g + 8
+    Scales<G, Z> sc[MT][2];
+    auto load_scales = [&](int unit) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                sc[m][h].load(M, at[m][h], unit * G, svec);
+                at[m][h] += G;
+            }
+    };
+    const char *col[NT];                         // XS: shared-memory offsets
+    uint4 x[NT][4];
+    auto load_x = [&](int half) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (XS) {
+                    // x_entry: words c of an odd column lie at c ^ 1
+                    const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(col[j]) +
+                                       half * P.half_stride + t * 16 + (c & 2) * 64 +
+                                       ((c & 1) ? 64 - ((g & 1) << 6) : (g & 1) << 6);
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(x[j][c].x), "=r"(x[j][c].y), "=r"(x[j][c].z), "=r"(x[j][c].w)
+                                 : "r"(a));
+                } else {
+                    x[j][c] = *reinterpret_cast<const uint4 *>(
+                        col[j] + (half * 16 + lane_word<VW>(t, c)) * 16);
+                }
+            }
+    };
+    auto start = [&](int job) {
+        P.begin(job);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) col[j] = P.col(j);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                at[m][h] = (int64_t)min(P.first_row(job, wr, m) + g + 8 * h, P.last_row(job, m)) * M.ng +
+                           u0 * G;
+        load_scales(u0);
+        if constexpr (!XS) load_x(2 * u0);
+    };
+
+    enter(0);
+    uint32_t stage = base;
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) issue(base + s * kStage);
+    P.ready();
+    start(0);
+    float acc[MT][NT][4] = {};
+    for (int job = 0, unit = u0;;) {
+        copy_wait<kStages - 1>();
+        __syncwarp();
+        Scales<G, Z> now[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) now[m][0] = sc[m][0], now[m][1] = sc[m][1];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t w[MT][2][4];
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t row = stage + m * 2048 + (8 * h + g) * 128;
+                    if constexpr (VW == 4) {
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[m][h][0]), "=r"(w[m][h][1]), "=r"(w[m][h][2]),
+                                       "=r"(w[m][h][3])
+                                     : "r"(row + (((half * 4 + t) ^ swz) << 4)));
+                    } else if constexpr (VW == 2) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                                         : "=r"(w[m][h][2 * q]), "=r"(w[m][h][2 * q + 1])
+                                         : "r"(row + (((half * 4 + 2 * q + (t >> 1)) ^ swz) << 4) +
+                                               (t & 1) * 8));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            asm volatile("ld.shared.u32 %0, [%1];"
+                                         : "=r"(w[m][h][q])
+                                         : "r"(row + (((half * 4 + q) ^ swz) << 4) + t * 4));
+                    }
+                }
+            if constexpr (XS) load_x(2 * unit + half);
+            if (half == 1) {
+                __syncwarp();
+                issue(stage);
+                stage = stage == base + (kStages - 1) * kStage ? base : stage + kStage;
+                if (unit + 1 < u1) load_scales(unit + 1);
+            }
+#pragma unroll
+            for (int gi = 0; gi < G / 2; ++gi) {
+                float c[MT][NT][4] = {};
+#pragma unroll
+                for (int v = 0; v < VW; ++v)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const ZeroPoint z0 = now[m][0].zero(half * (G / 2) + gi),
+                                        z1 = now[m][1].zero(half * (G / 2) + gi);
+                        const uint32_t w0 = w[m][0][gi * VW + v], w1 = w[m][1][gi * VW + v];
+                        const uint32_t a0[4] = {code_pair0(w0, z0), code_pair0(w1, z1),
+                                                code_pair1(w0, z0), code_pair1(w1, z1)};
+                        const uint32_t a1[4] = {code_pair0(w0 >> 8, z0), code_pair0(w1 >> 8, z1),
+                                                code_pair1(w0 >> 8, z0), code_pair1(w1 >> 8, z1)};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const uint4 b = x[j][gi * VW + v];
+                            mma16816(c[m][j], a0, b.x, b.y);
+                            mma16816(c[m][j], a1, b.z, b.w);
+                        }
+                    }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const float s0 = now[m][0].scale(half * (G / 2) + gi),
+                                s1 = now[m][1].scale(half * (G / 2) + gi);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        acc[m][j][0] += s0 * c[m][j][0];
+                        acc[m][j][1] += s0 * c[m][j][1];
+                        acc[m][j][2] += s1 * c[m][j][2];
+                        acc[m][j][3] += s1 * c[m][j][3];
+                    }
+                }
+            }
+            if constexpr (!XS)
+                if (half == 0 || unit + 1 < u1) load_x(2 * unit + half + 1);
+        }
+        if (++unit < u1) continue;
+        P.end(job, acc);
+        unit = u0;
+        if (++job == P.jobs) return;
+        start(job);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+    }
+}
+
+// The warps' sums of a job side by side in shared memory: v[warp][row][column].
+template <int MT, int NT>
+struct Red {
+    float v[kWarps][16 * MT][8 * NT + 1];
+    __device__ __forceinline__ void put(const float (&acc)[MT][NT][4]) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[warp][16 * i + 8 * (e >> 1) + (lane >> 2)][8 * j + 2 * (lane & 3) + (e & 1)] =
+                        acc[i][j][e];
+    }
+    // Sum over the WK warps of row group wr of columns c .. c + terms - 1 (the terms of one
+    // value, small first).
+    __device__ __forceinline__ float sum(int wr, int WK, int r, int c, int terms) const {
+        float s = 0.f;
+        for (int t = terms - 1; t >= 0; --t) {
+            const float *p = &v[wr * WK][r][c + t];
+            for (int w = 0; w < WK; ++w) s += p[w * (16 * MT) * (8 * NT + 1)];
+        }
+        return kCodeUnit * s;
+    }
+};
+
 // ---------------------------------------------------------------------------------
 // Host: launchers
 // ---------------------------------------------------------------------------------
@@ -190,10 +475,10 @@ cudaError_t quantize(const void *W, int w_bf16, int64_t m, int64_t n, const floa
                      int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z, cudaStream_t st);
 cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf16,
                        cudaStream_t st);
-// xt: the split columns of FP32 X ([B][kTerms][ldx], ldx = split_ld(n)), unused for BF16.
-NQ_HD int64_t split_ld(int64_t n) { return round_up(n, 8); }
+// xw: workspace for the columns of X in word order (x_workspace bytes).
+size_t x_workspace(int64_t n, int x_bf16, int64_t B);
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
-                   float *Y, __nv_bfloat16 *xt, cudaStream_t st);
+                   float *Y, __nv_bfloat16 *xw, cudaStream_t st);
 
 
 // Expert layer for a few tokens (moe.cu).
@@ -205,11 +490,12 @@ struct MoeArgs {
     Mat gate_up;               // E matrices of 2f x d, one after the other
     Mat down;                  // E matrices of d x f
     int group;
+    int svec_gate_up, svec_down;   // set by moe()
     float *Y;                  // [B][d]
     int32_t *ids;              // [B][top_k]
     float *weights;            // [B][top_k]
-    __nv_bfloat16 *xt;         // [B][kTerms][split_ld(d)] (FP32 X)
-    __nv_bfloat16 *h;          // [B top_k][kTerms][split_ld(f)]
+    __nv_bfloat16 *xw;         // [B][1 or kTerms][padded(d)], word order
+    __nv_bfloat16 *h;          // [B top_k][kTerms][padded(f)], word order
 };
 cudaError_t moe(const MoeArgs &a, cudaStream_t st);
 

@@ -216,7 +216,8 @@ def test_wrappers_refuse_what_does_not_fit(nq):
     with pytest.raises(ValueError):
         nq.nq_w4_matmul(packed, scales, X, group=32, ws=torch.empty(64, device="cuda"))
     with pytest.raises(nq.NQError):
-        nq.nq_w4_matmul(packed, scales, X, group=32, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        nq.nq_w4_matmul(packed, scales, torch.zeros(99, 64, device="cuda"), group=32,
+                        ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(nq.NQError):
         nq.nq_w4_quantize(X, group=32, grid=0)
     with pytest.raises(ValueError):

@@ -32,7 +32,7 @@ def test_dequantize_refuses():
 
 
 def test_matmul_refuses():
-    def call(packed=FAKE, scales=FAKE, m=8, n=64, group=32, X=FAKE, dt=0, B=2, Y=FAKE, ws=FAKE,
+    def call(packed=FAKE, scales=FAKE, m=8, n=64, group=32, X=FAKE, dt=0, B=99, Y=FAKE, ws=FAKE,
              ws_bytes=1 << 30):
         return L.nq_w4_matmul(packed, scales, None, m, n, group, X, dt, B, Y, ws, ws_bytes, None)
     for bad in (dict(packed=None), dict(packed=FAKE + 8), dict(scales=None), dict(m=0), dict(n=0),
