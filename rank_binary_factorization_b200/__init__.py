@@ -172,32 +172,42 @@ def nq_pack_signs(X):
     return bits
 
 
+_DTYPES = {torch.float32: NQ_F32, torch.bfloat16: NQ_BF16}
+# handle of the current stream of a device (torch.cuda.current_stream builds an object each time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _w4_call(fn, dev, *args):
     """Call a library function on the current stream of device ``dev``."""
     if dev == torch.cuda.current_device():
-        code = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
+        code = getattr(lib, fn)(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = getattr(lib, fn)(*args, torch.cuda.current_stream(dev).cuda_stream)
+            code = getattr(lib, fn)(*args, _raw_stream(dev))
     if code != _lib.NQ_OK:
         raise NQError(fn, code)
 
 
-def _w4_layer(what, packed, scales, zeros, rows, n, group, dev):
-    """Check one packed array: ``rows`` rows (its leading dimensions) of ``n`` columns."""
-    if group not in (32, 64, 128):
+def _w4_group(group):
+    if group != 128 and group != 64 and group != 32:
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
-    ld, ng = (n + 31) // 32 * 4, (n + group - 1) // group
-    for t, dt, width, name in ((packed, torch.int32, ld, ""), (scales, torch.bfloat16, ng, " scales"),
-                               (zeros, torch.uint8, ng, " zeros")):
-        if t is None and name == " zeros":
-            continue
-        if t.dtype != dt:
-            raise TypeError(f"{what}{name} must be {dt}, got {t.dtype}")
-        if tuple(t.shape) != (*rows, width):
-            raise ValueError(f"{what}{name} must have shape {(*rows, width)}, got {tuple(t.shape)}")
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError(f"{what}{name} must be contiguous and on the device of the input")
+
+
+def _w4_layer(what, packed, scales, zeros, rows, n, group, dev):
+    """Check one packed array: ``rows`` (its leading dimensions) rows of ``n`` columns."""
+    _w4_group(group)
+    words, groups = rows + ((n + 31) // 32 * 4,), rows + ((n + group - 1) // group,)
+    if packed.dtype != torch.int32 or scales.dtype != torch.bfloat16 or \
+            zeros is not None and zeros.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes must be int32, scales bfloat16 and zeros uint8")
+    if packed.shape != words or scales.shape != groups or zeros is not None and zeros.shape != groups:
+        raise ValueError(f"{what}: {n} columns in groups of {group} need codes of shape {words}, "
+                         f"scales and zeros of shape {groups}")
+    for t in (packed, scales, zeros):
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"{what}: codes, scales and zeros must be contiguous and on the "
+                             "device of the input")
 
 
 def _w4_input(x, name, dims):
@@ -207,14 +217,17 @@ def _w4_input(x, name, dims):
         raise ValueError(f"{name} has {x.dim()} dimensions")
     if x.numel() == 0:
         raise ValueError(f"{name} is empty")
-    return x.get_device(), _dtype(x)
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {x.dtype}: use float32 or bfloat16")
+    return x.get_device(), dt
 
 
 def _w4_ws(ws, need, dev):
     if ws is None:
         if need == 0:
             return None, 0
-        ws = workspace(need, dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
     elif ws.get_device() != dev or not ws.is_contiguous() or ws.element_size() != 1:
         raise ValueError("ws must be a contiguous byte tensor on the device of the input")
     return ws.data_ptr(), ws.numel()
@@ -229,15 +242,14 @@ def nq_w4_quantize(W, group=128, d_in=None, symmetric=True, grid=1):
     """
     dev, dt = _w4_input(W, "W", (2,))
     m, n = W.shape
-    if group not in (32, 64, 128):
-        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    _w4_group(group)
     if d_in is not None and not (d_in.get_device() == dev and d_in.dtype == torch.float32 and
                                  d_in.is_contiguous() and tuple(d_in.shape) == (n,)):
         raise ValueError("d_in must be a contiguous float32 vector of length n on W's device")
     ng = (n + group - 1) // group
-    packed = torch.empty(m, (n + 31) // 32 * 4, dtype=torch.int32, device=W.device)
-    scales = torch.empty(m, ng, dtype=torch.bfloat16, device=W.device)
-    zeros = None if symmetric else torch.empty(m, ng, dtype=torch.uint8, device=W.device)
+    packed = W.new_empty((m, (n + 31) // 32 * 4), dtype=torch.int32)
+    scales = W.new_empty((m, ng), dtype=torch.bfloat16)
+    zeros = None if symmetric else W.new_empty((m, ng), dtype=torch.uint8)
     _w4_call("nq_w4_quantize", dev, W.data_ptr(), dt, m, n,
              None if d_in is None else d_in.data_ptr(), group, grid, packed.data_ptr(),
              scales.data_ptr(), None if zeros is None else zeros.data_ptr())
@@ -250,7 +262,7 @@ def nq_w4_dequantize(packed, scales, n, group=128, zeros=None, dtype=torch.float
         raise ValueError("packed must be a non-empty two-dimensional CUDA tensor and n positive")
     dev, m = packed.get_device(), packed.shape[0]
     _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
-    W = torch.empty(m, n, dtype=dtype, device=packed.device)
+    W = packed.new_empty((m, n), dtype=dtype)
     _w4_call("nq_w4_dequantize", dev, packed.data_ptr(), scales.data_ptr(),
              None if zeros is None else zeros.data_ptr(), m, n, group, W.data_ptr(), _dtype(W))
     return W
@@ -263,7 +275,7 @@ def nq_w4_matmul(packed, scales, X, group=128, zeros=None, ws=None):
     B = X.shape[0] if X.dim() == 2 else 1
     m = packed.shape[0]
     _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
-    Y = torch.empty((B, m) if X.dim() == 2 else (m,), dtype=torch.float32, device=X.device)
+    Y = X.new_empty((B, m) if X.dim() == 2 else (m,), dtype=torch.float32)
     ws_ptr, ws_bytes = _w4_ws(ws, lib.nq_w4_workspace_size(m, n, dt, B), dev)
     _w4_call("nq_w4_matmul", dev, packed.data_ptr(), scales.data_ptr(),
              None if zeros is None else zeros.data_ptr(), m, n, group, X.data_ptr(), dt, B,
@@ -289,11 +301,11 @@ def nq_moe_w4(X, router, gate_up, gate_up_scales, down, down_scales, top_k, grou
         raise ValueError(f"router must be a contiguous {X.dtype} tensor of shape {(E, d)} on X's device")
     _w4_layer("gate_up", gate_up, gate_up_scales, gate_up_zeros, (E, 2 * f), d, group, dev)
     _w4_layer("down", down, down_scales, down_zeros, (E, d), f, group, dev)
-    Y = torch.empty(B, d, dtype=torch.float32, device=X.device)
+    Y = X.new_empty((B, d), dtype=torch.float32)
     ids = weights = None
     if want_routing:
-        ids = torch.empty(B, top_k, dtype=torch.int32, device=X.device)
-        weights = torch.empty(B, top_k, dtype=torch.float32, device=X.device)
+        ids = X.new_empty((B, top_k), dtype=torch.int32)
+        weights = X.new_empty((B, top_k), dtype=torch.float32)
     need = lib.nq_moe_workspace_size(B, d, f, E, top_k, dt)
     if need == 0:
         raise NQError("nq_moe_workspace_size", _lib.NQ_ERR_INVALID_ARG)

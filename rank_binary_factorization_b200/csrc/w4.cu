@@ -13,9 +13,18 @@ namespace w4 {
 // and the lowest candidate with the least E is kept.  A lane holds 16 consecutive columns,
 // g / 16 lanes a group; the scale and z are formed in FP64 (the scale then rounded to FP32
 // and to BF16), rint(w / s) is that of the exact quotient (ties to even) and E is summed in
-// FP64, so that neither a border case nor the choice depends on the order of operations.
+// FP64 where it matters, so that neither a border case nor the choice depends on the order of
+// operations.
+//
+// The search runs in FP32 (six FMA-pipe operations a column and candidate: the clamp is the
+// saturation of an FMA in units of 15 steps) and is off by less than 2.7e-5 of E (16 roundings of
+// a term and of the sum, 1e-6; a column within 3.2e-6 steps of a half that rounds the other way,
+// 2.6e-5 of its term); a candidate within kNear of the best so far is settled in FP64, both of
+// them anew (about one comparison in 10000).
 // ---------------------------------------------------------------------------------
-constexpr int kPer = 16;   // columns per lane
+constexpr int kPer = 16;            // columns per lane
+constexpr float kNear = 6e-5f;
+constexpr float kMagic = 12582912.f;   // 1.5 2^23: adding it leaves rint(x) in the low bits
 
 // rint(w / s) of the exact quotient, ties to even, exact for |w / s| <= 16 (larger
 // magnitudes come out beyond +-15).  w - a s is exact in FP32 for the nearest integers a
@@ -29,114 +38,225 @@ __device__ __forceinline__ float exact_rint(float w, float s, float inv) {
     return a;
 }
 
+// Maxima that hand on a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
 template <int LPG>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-    for (int o = LPG / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = LPG / 2; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-template <int LPG>
-__device__ __forceinline__ double group_sum(double v) {
+template <int LPG, typename T>
+__device__ __forceinline__ T group_sum(T v) {
 #pragma unroll
     for (int o = LPG / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+
+// x / c in FP64 for a quotient far from the ends of its range, r about 1 / c: the residual of
+// the first quotient is exact and corrects it to the rounded one.
+__device__ __forceinline__ double quotient(double x, double c, double r) {
+    const double q = x * r;
+    return fma(fma(-q, c, x), r, q);
 }
 
 // Scale (a BF16 value) and zero point of a candidate.
 __device__ __forceinline__ void candidate(double alpha, float lo, float hi, bool zeros, float &s,
                                           float &z) {
     if (zeros) {
-        s = bf16_round((float)(alpha * ((double)hi - (double)lo) / 15.0));
-        z = s > 0.f ? (float)fmin(fmax(rint(-alpha * (double)lo / (double)s), 0.0), 15.0) : 0.f;
+        s = bf16_round((float)quotient(alpha * ((double)hi - (double)lo), 15.0, 1.0 / 15.0));
+        const double x = -alpha * (double)lo, c = (double)s;
+        double v;
+        if (s > 0x1p-100f && s < 0x1p100f) {
+            const double r0 = (double)__frcp_rn(s);
+            v = quotient(x, c, fma(fma(-c, r0, 1.0), r0, r0));
+        } else {
+            v = x / c;
+        }
+        z = s > 0.f ? (float)fmin(fmax(rint(v), 0.0), 15.0) : 0.f;
     } else {
-        s = bf16_round((float)(alpha * (double)hi / 7.0));
+        s = bf16_round((float)quotient(alpha * (double)hi, 7.0, 1.0 / 7.0));
         z = 8.f;
     }
 }
 
-// Codes of the lane's columns for scale s: v[i] = q - z (so W^ = s v).
-__device__ __forceinline__ void round_codes(const float (&w)[kPer], float s, float z,
-                                            float (&v)[kPer]) {
-    // a scale next to the least normal number: both sides moved up by 2^100, exactly
-    const float up = s < 0x1p-100f ? 0x1p100f : 1.f;
-    const float su = s * up, inv = 1.f / su;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        v[i] = s > 0.f ? fminf(fmaxf(exact_rint(w[i] * up, su, inv), -z), 15.f - z) : 0.f;
+// Exact q - z of one column (so w^ = s (q - z)).  ``up`` moves a scale next to the least normal
+// number away from it, exactly, together with w.
+__device__ __forceinline__ float scale_up(float s) { return s < 0x1p-100f ? 0x1p100f : 1.f; }
+__device__ __forceinline__ float exact_code(float w, float s, float z, float up) {
+    const float su = s * up;
+    return s > 0.f ? fminf(fmaxf(exact_rint(w * up, su, 1.f / su), -z), 15.f - z) : 0.f;
 }
 
-template <int LPG, typename T>
-__global__ void __launch_bounds__(256)
-    quantize_kernel(const T *__restrict__ W, int64_t m, int n, const float *__restrict__ d_in,
-                    int grid, int vec, int ld, int ng, uint32_t *__restrict__ q,
-                    __nv_bfloat16 *__restrict__ sc, uint8_t *__restrict__ zp) {
-    const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int per_row = ng * LPG;
-    const int64_t row = unit / per_row;
-    const int u = (int)(unit % per_row);
-    const bool live = row < m;          // whole groups: a group's lanes share a row
-    const int k0 = u * kPer;
-    const bool zeros = zp != nullptr;
-    float w[kPer];
-    const T *src = W + (live ? row : 0) * n + k0;
+// The lane's part of E in FP64.
+__device__ __forceinline__ double exact_error(const float (&w)[kPer], const float (&d)[kPer], float s,
+                                           float z) {
+    const float up = scale_up(s);
+    double e = 0.0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) w[i] = 0.f;
-    if (live && vec && k0 + kPer <= n) {
+    for (int i = 0; i < kPer; ++i) {
+        const double t = ((double)w[i] - (double)s * (double)exact_code(w[i], s, z, up)) * (double)d[i];
+        e += t * t;
+    }
+    return e;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_per(const T *src, int k0, int n, bool vec, float (&v)[kPer]) {
+    if (vec && k0 + kPer <= n) {
         constexpr int NV = kPer * sizeof(T) / 16;
         uint4 raw[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
+        for (int i = 0; i < NV; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + k0) + i);
         const T *h = reinterpret_cast<const T *>(raw);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) w[i] = (float)h[i];
-    } else if (live) {
+        for (int i = 0; i < kPer; ++i) v[i] = (float)h[i];
+    } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (k0 + i < n) w[i] = (float)src[i];
+        for (int i = 0; i < kPer; ++i) v[i] = k0 + i < n ? (float)src[k0 + i] : 0.f;
     }
-    float lo = 0.f, hi = 0.f;
-    bool bad = false;
+}
+
+// lo = min(0, min w) and hi = max(0, max w) (without zeros: hi = max |w|); NaN in hi if in w.
+__device__ __forceinline__ void range_of(const float (&w)[kPer], bool zeros, float &lo, float &hi) {
+    lo = hi = 0.f;
+    if (zeros) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        bad |= !isfinite(w[i]);
-        lo = fminf(lo, w[i]);
-        hi = fmaxf(hi, w[i]);
+        for (int i = 0; i < kPer; ++i) {
+            lo = fminf(lo, w[i]);
+            hi = max_nan(hi, w[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) hi = max_nan(hi, fabsf(w[i]));
     }
-    if (!zeros) hi = fmaxf(hi, -lo);
+}
+
+// A row is worked on by 2^ltpr lanes (LPG to a group) side by side, blockIdx.y of them after one
+// another along the row.
+template <int LPG, bool SEARCH, typename T>
+__global__ void __launch_bounds__(256)
+    quantize_kernel(const T *__restrict__ W, int64_t m, int n, const float *__restrict__ d_in,
+                    int grid, int vec, int dvec, int ltpr, int ld, int ng, uint32_t *__restrict__ q,
+                    __nv_bfloat16 *__restrict__ sc, uint8_t *__restrict__ zp) {
+    const int64_t row = ((int64_t)blockIdx.x << (8 - ltpr)) + (threadIdx.x >> ltpr);
+    const int u = ((int)blockIdx.y << ltpr) + (threadIdx.x & ((1 << ltpr) - 1));
+    const bool live = row < m && u < ng * LPG;          // whole groups
+    const int k0 = u * kPer;
+    const bool zeros = zp != nullptr;
+    float w[kPer], lo, hi;
+    load_per(W + (live ? row * n : 0), live ? k0 : n, n, vec, w);
+    range_of(w, zeros, lo, hi);
     hi = group_max<LPG>(hi);
     lo = -group_max<LPG>(-lo);
-    bad = group_max<LPG>(bad ? 1.f : 0.f) > 0.f;
+    const bool nan = !(hi - lo < __int_as_float(0x7f800000));    // a weight that is not finite
 
     float s, z;
-    candidate(1.0, lo, hi, zeros, s, z);
-    if (grid > 1) {
-        double best = 0.0;
-        int pick = 0;
-        for (int c = 0; c < grid; ++c) {
-            float cs, cz, v[kPer];
-            candidate(1.0 - c / (2.0 * grid), lo, hi, zeros, cs, cz);
-            round_codes(w, cs, cz, v);
-            double e = 0.0;
+    if constexpr (!SEARCH) {
+        candidate(1.0, lo, hi, zeros, s, z);
+    } else {
+        float d[kPer];
+        if (d_in) {
+            load_per(d_in, live ? k0 : n, n, dvec, d);
+        } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const double d = d_in && k0 + i < n ? (double)d_in[k0 + i] : 1.0;
-                const double t = ((double)w[i] - (double)cs * (double)v[i]) * d;
-                e += t * t;
-            }
-            e = group_sum<LPG>(e);
-            if (c == 0 || e < best) best = e, pick = c;
+            for (int i = 0; i < kPer; ++i) d[i] = 1.f;
         }
-        candidate(1.0 - pick / (2.0 * grid), lo, hi, zeros, s, z);
+        // outside this range of weights and errors every candidate is settled in FP64
+        const bool plain = hi - lo > 1e-25f && hi - lo < 1e25f;
+        float best = 0.f, bs = 0.f, bz = 0.f;
+        double best64 = -1.0;                           // E of the best in FP64 once needed
+        const int sub = threadIdx.x & (LPG - 1);
+        for (int c0 = 0; c0 < grid; c0 += LPG) {
+            float ms, mz;                               // lane ``sub`` forms candidate c0 + sub
+            candidate(1.0 - (c0 + sub) / (2.0 * grid), lo, hi, zeros, ms, mz);
+            const float minv = 1.f / (15.f * ms);
+            for (int j = 0; j < min(LPG, grid - c0); ++j) {
+                const int from = (threadIdx.x & 31 & ~(LPG - 1)) | j;
+                const float cs = __shfl_sync(0xffffffffu, ms, from),
+                            cz = __shfl_sync(0xffffffffu, mz, from),
+                            inv = __shfl_sync(0xffffffffu, minv, from);
+                const float z15 = cz * (1.f / 15.f), off = kMagic + cz;
+                float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPer; i += 2) {
+                    const float v0 = fmaf(__saturatef(fmaf(w[i], inv, z15)), 15.f, kMagic) - off,
+                                v1 = fmaf(__saturatef(fmaf(w[i + 1], inv, z15)), 15.f, kMagic) - off;
+                    const float t0 = fmaf(-cs, v0, w[i]) * d[i], t1 = fmaf(-cs, v1, w[i + 1]) * d[i + 1];
+                    e0 = fmaf(t0, t0, e0);
+                    e1 = fmaf(t1, t1, e1);
+                }
+                const float e = group_sum<LPG>(e0 + e1);
+                const bool first = c0 + j == 0;
+                const bool safe = plain && e > 1e-30f && best > 1e-30f && best < 1e30f;
+                bool less = first || (safe && e < best * (1.f - kNear));
+                const bool near = !first && !less && !(safe && e > best * (1.f + kNear));
+                if (__any_sync(0xffffffffu, near)) {
+                    const double a = group_sum<LPG>(exact_error(w, d, bs, bz));
+                    const double b = group_sum<LPG>(exact_error(w, d, cs, cz));
+                    if (near) {
+                        if (best64 < 0.0) best64 = a;
+                        less = b < best64;
+                        if (less) best64 = b;
+                    } else if (less) {
+                        best64 = -1.0;
+                    }
+                } else if (less) {
+                    best64 = -1.0;
+                }
+                if (less) best = e, bs = cs, bz = cz;
+            }
+        }
+        s = bs, z = bz;
     }
     // a group with a weight that is not finite reads back as NaN
-    if (bad) s = __int_as_float(0x7fc00000), z = zeros ? 0.f : 8.f;
-    float v[kPer];
-    round_codes(w, s, z, v);
-    if (!live) return;
-    uint32_t word[2] = {0, 0};
+    if (nan) s = __int_as_float(0x7fc00000), z = zeros ? 0.f : 8.f;
+    uint32_t word[2];
+    {
+        // t = w / s, rounded correctly (quotient and one correction, so a half comes out as the
+        // half and goes to even); a = rint(t) from the low bits of + kMagic.  The remainder
+        // w - a s is exact: beyond half a step t was off a half by less than its last bit, and
+        // the lane settles its columns one by one.
+        const float inv = 1.f / s, z15 = z * (1.f / 15.f);
+        float dev = 0.f;
+        uint32_t acc[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        if (k0 + i < n) word[i / 8] |= (uint32_t)(int)(v[i] + z) << (4 * (i % 8));
+        for (int i = kPer - 1; i >= 0; --i) {
+            const float t0 = w[i] * inv, t = fmaf(fmaf(-t0, s, w[i]), inv, t0);
+            const float a = (t + kMagic) - kMagic;
+            dev = fmaxf(dev, fabsf(fmaf(-a, s, w[i])));
+            // clamped to 0 .. 15 in units of 15, and back
+            const float c = fmaf(__saturatef(fmaf(a, 1.f / 15.f, z15)), 15.f, kMagic);
+            acc[i / 8] = acc[i / 8] * 16u + __float_as_uint(c);
+        }
+        // the eight codes carry the bits of kMagic each
+        word[0] = acc[0] - 0x4b400000u * 0x11111111u;
+        word[1] = acc[1] - 0x4b400000u * 0x11111111u;
+        // (also where s is 0, NaN, or so small that 1 / s or a remainder is not exact)
+        if (!(s > 0x1p-100f) || !(dev <= 0.5f * s)) {
+            const float up = scale_up(s);
+            word[0] = word[1] = 0;
+#pragma unroll 1
+            for (int i = 0; i < kPer; ++i) {
+                float wi = 0.f;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j == i) wi = w[j];
+                const float v = exact_code(wi, s, z, up);
+                word[i >> 3] |= (uint32_t)(int)(v + z) << (4 * (i & 7));
+            }
+        }
+    }
+    if (!live) return;
+    if (k0 + kPer > n) {                                // codes past the last column are 0
+        const int left = n - k0;
+        word[0] = left <= 0 ? 0 : left < 8 ? word[0] & ((1u << 4 * left) - 1) : word[0];
+        word[1] = left <= 8 ? 0 : word[1] & ((1u << 4 * (left - 8)) - 1);
+    }
     const int wi = u * 2;
     if (wi < ld) *reinterpret_cast<uint2 *>(q + row * ld + wi) = make_uint2(word[0], word[1]);
     if (u % LPG == 0) {
@@ -146,19 +266,33 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// log2 of the lanes of a row: a power of two that covers ``units``, at least ``least``, at most 256.
+static int row_lanes(int64_t units, int least) {
+    int l = least;
+    while (l < 8 && (1 << l) < units) ++l;
+    return l;
+}
+
 template <int LPG>
 static cudaError_t quantize_t(const void *W, int w_bf16, int64_t m, int64_t n, const float *d_in,
                               int group, int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z,
                               cudaStream_t st) {
     const int ld = (int)row_words(n), ng = (int)row_groups(n, group);
-    const int64_t blocks = ceil_div(m * (int64_t)ng * LPG, 256);
+    const int ltpr = row_lanes(ng * LPG, LPG == 8 ? 3 : LPG == 4 ? 2 : 1);
+    const dim3 blocks((unsigned)ceil_div(m, 256 >> ltpr), (unsigned)ceil_div(ng * LPG, 1 << ltpr));
     const int vec = n % (w_bf16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
+    const int dvec = reinterpret_cast<uintptr_t>(d_in) % 16 == 0;
+    auto run = [&](auto kern, auto *src) {
+        kern<<<blocks, 256, 0, st>>>(src, m, (int)n, d_in, grid, vec, dvec, ltpr, ld, ng, q, s, z);
+    };
+    const __nv_bfloat16 *wb = static_cast<const __nv_bfloat16 *>(W);
+    const float *wf = static_cast<const float *>(W);
     if (w_bf16)
-        quantize_kernel<LPG, __nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(
-            static_cast<const __nv_bfloat16 *>(W), m, (int)n, d_in, grid, vec, ld, ng, q, s, z);
+        grid > 1 ? run(quantize_kernel<LPG, true, __nv_bfloat16>, wb)
+                 : run(quantize_kernel<LPG, false, __nv_bfloat16>, wb);
     else
-        quantize_kernel<LPG, float><<<(unsigned)blocks, 256, 0, st>>>(
-            static_cast<const float *>(W), m, (int)n, d_in, grid, vec, ld, ng, q, s, z);
+        grid > 1 ? run(quantize_kernel<LPG, true, float>, wf)
+                 : run(quantize_kernel<LPG, false, float>, wf);
     count_launch();
     return cudaGetLastError();
 }
@@ -172,48 +306,54 @@ cudaError_t quantize(const void *W, int w_bf16, int64_t m, int64_t n, const floa
 
 // ---------------------------------------------------------------------------------
 // Read-back: W^ = s (q - z), exact in FP32 (12 significant bits), rounded once for BF16.
-// One lane per word (8 columns).
+// A lane reads two words (16 columns of one group).
 // ---------------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(256)
-    dequantize_kernel(const Mat M, int64_t m, int wpg, int vec, T *__restrict__ out) {
-    const int nw = (M.n + 7) / 8;
-    const int64_t unit = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t row = unit / nw;
-    const int word = (int)(unit % nw);
-    if (row >= m) return;
-    const uint32_t w = __ldcs(M.q + row * M.ld + word);
-    const int64_t at = row * M.ng + word / wpg;
+    dequantize_kernel(const Mat M, int64_t m, int upg, int vec, int ltpr, T *__restrict__ out) {
+    const int64_t row = ((int64_t)blockIdx.x << (8 - ltpr)) + (threadIdx.x >> ltpr);
+    const int u = ((int)blockIdx.y << ltpr) + (threadIdx.x & ((1 << ltpr) - 1));
+    const int k0 = u * kPer;
+    if (row >= m || k0 >= M.n) return;
+    const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(M.q + row * M.ld + 2 * u));
+    const int64_t at = row * M.ng + u / upg;
     const float s = __bfloat162float(M.s[at]);
-    const float z = M.z ? (float)(__ldg(M.z + at) & 15) : 8.f;
-    T v[8];
+    // the code in the low mantissa bits of 2^23
+    const float off = 8388608.f + (M.z ? (float)(__ldg(M.z + at) & 15) : 8.f);
+    T v[kPer];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (T)(s * ((float)((w >> (4 * i)) & 15u) - z));
-    T *dst = out + row * M.n + word * 8;
-    if (vec) {
-        constexpr int NV = 8 * sizeof(T) / 16;
+    for (int i = 0; i < kPer; ++i) {
+        const uint32_t c = ((i < 8 ? w.x : w.y) >> (4 * (i & 7))) & 15u;
+        v[i] = (T)(s * (__uint_as_float(0x4b000000u | c) - off));
+    }
+    T *dst = out + row * M.n + k0;
+    if (vec && k0 + kPer <= M.n) {
+        constexpr int NV = kPer * sizeof(T) / 16;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             __stcs(reinterpret_cast<uint4 *>(dst) + i, reinterpret_cast<const uint4 *>(v)[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (word * 8 + i < M.n) dst[i] = v[i];
+        for (int i = 0; i < kPer; ++i)
+            if (k0 + i < M.n) dst[i] = v[i];
     }
+}
+
+template <typename T>
+static cudaError_t dequantize_t(const Mat &M, int64_t m, int group, T *out, cudaStream_t st) {
+    const int64_t units = ceil_div(M.n, kPer);
+    const int ltpr = row_lanes(units, 0);
+    const dim3 blocks((unsigned)ceil_div(m, 256 >> ltpr), (unsigned)ceil_div(units, 1 << ltpr));
+    const int vec = (M.n * sizeof(T)) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    dequantize_kernel<T><<<blocks, 256, 0, st>>>(M, m, group / kPer, vec, ltpr, out);
+    count_launch();
+    return cudaGetLastError();
 }
 
 cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf16,
                        cudaStream_t st) {
-    const int64_t blocks = ceil_div(m * ceil_div(M.n, 8), 256);
-    const int vec = M.n % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    if (out_bf16)
-        dequantize_kernel<<<(unsigned)blocks, 256, 0, st>>>(M, m, group / 8, vec,
-                                                           static_cast<__nv_bfloat16 *>(out));
-    else
-        dequantize_kernel<<<(unsigned)blocks, 256, 0, st>>>(M, m, group / 8, vec,
-                                                           static_cast<float *>(out));
-    count_launch();
-    return cudaGetLastError();
+    if (out_bf16) return dequantize_t(M, m, group, static_cast<__nv_bfloat16 *>(out), st);
+    return dequantize_t(M, m, group, static_cast<float *>(out), st);
 }
 
 // ---------------------------------------------------------------------------------
