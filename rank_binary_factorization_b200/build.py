@@ -10,8 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnq.so")
 SOURCES = ["api.cu", "gemm_tc.cu", "kernels.cu", "chol.cu", "binary.cu", "calib_noalloc.cu",
-           "selftest.cu", "w4.cu", "moe.cu"]
-HEADERS = ["common.cuh", "gemm_tc.cuh", "kernels.cuh", "layout.h", "w4.cuh",
+           "selftest.cu", "w4.cu", "w4_tc.cu", "moe.cu"]
+HEADERS = ["common.cuh", "gemm_tc.cuh", "kernels.cuh", "layout.h", "tc_ptx.cuh", "w4.cuh",
            os.path.join("..", "..", "include", "nq.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-shared", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"]

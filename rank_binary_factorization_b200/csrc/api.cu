@@ -1420,7 +1420,7 @@ nq_status nq_w4_dequantize(const uint32_t *packed, const void *scales, const uin
 size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B) {
     if (m < 1 || n < 1 || B < 1 || m > w4::kMaxRows || n > kMaxDim || B > kMaxDim || !dtype_ok(dt))
         return 0;
-    return align_up(w4::x_workspace(n, dt == NQ_BF16, B));
+    return align_up(w4::matmul_workspace(m, n, dt == NQ_BF16, B));
 }
 
 nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,

@@ -467,9 +467,17 @@ static bool x_shared(int64_t n, int x_bf16, int64_t B) {
     return cols <= 8 && cols * padded(n) * 2 <= kXsBytes;
 }
 
-size_t x_workspace(int64_t n, int x_bf16, int64_t B) {
+// Rows of X from which the tensor-memory path (w4_tc.cu) takes the call.
+constexpr int64_t kTcRows = 17;
+
+static size_t x_bytes(int64_t n, int x_bf16, int64_t B) {
+    const size_t b = (size_t)B * (x_bf16 ? 1 : kTerms) * padded(n) * 2;
+    return (b + 255) / 256 * 256;
+}
+
+size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B) {
     if (x_shared(n, x_bf16, B)) return 0;
-    return (size_t)B * (x_bf16 ? 1 : kTerms) * padded(n) * 2;
+    return x_bytes(n, x_bf16, B) + (B >= kTcRows ? tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes : 0);
 }
 
 template <int VW, bool Z, bool XS, int MT, int NT>
@@ -508,6 +516,10 @@ cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16
             X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw));
         count_launch();
     }
+    if (B >= kTcRows)
+        return tc_matmul(M, m, group, xw, x_bf16 ? 1 : kTerms, B, Y,
+                         reinterpret_cast<float *>(reinterpret_cast<char *>(xw) + x_bytes(M.n, x_bf16, B)),
+                         st);
     auto run = M.z ? (group == 32 ? gemv<1, true> : group == 64 ? gemv<2, true> : gemv<4, true>)
                    : (group == 32 ? gemv<1, false> : group == 64 ? gemv<2, false> : gemv<4, false>);
     return run(M, m, X, x_bf16, xw, B, Y, st);

@@ -475,11 +475,22 @@ cudaError_t quantize(const void *W, int w_bf16, int64_t m, int64_t n, const floa
                      int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z, cudaStream_t st);
 cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf16,
                        cudaStream_t st);
-// xw: workspace for the columns of X in word order (x_workspace bytes).
-size_t x_workspace(int64_t n, int x_bf16, int64_t B);
+// xw: workspace (matmul_workspace bytes) for the columns of X in word order and the parts of a
+// split k axis.
+size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B);
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st);
 
+
+// Many rows of X on tcgen05 (w4_tc.cu).
+struct TcPlan {
+    int BN;                    // rows of X of a tile
+    int parts, part_units;     // parts of the k axis, units of kUnit columns of a part
+    size_t partial_bytes;      // their sums ([parts][B][m]) if there is more than one
+};
+TcPlan tc_plan(int64_t m, int64_t n, int terms, int64_t B);
+cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *xw, int terms, int64_t B,
+                      float *Y, float *partial, cudaStream_t st);
 
 // Expert layer for a few tokens (moe.cu).
 struct MoeArgs {

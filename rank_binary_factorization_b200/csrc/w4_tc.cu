@@ -1,0 +1,423 @@
+// Product of a 4-bit layer with many rows of X on tcgen05 (sm_100a): Y^T = W^ X^T in tiles of
+// 128 rows of W and BN rows of X.
+//
+// D = sum over k of (q - z) x is formed per group of g columns on the tensor cores, from exact
+// operands (small integers in BF16; X in BF16, or FP32 as kTerms BF16 terms that share one
+// operand), and drained group by group into FP32 registers as acc += s D: the scale of a row
+// is one FMA of the drain, no product is rounded before the sum, and a sum in the tensor core
+// never runs longer than a group.  At g = 128 and BN = 128 a drain costs 128 FMAs a thread
+// against 512 clocks of MMA.
+//
+// Persistent, one CTA an SM, fourteen warps around one ring of kRing stages of 128 columns of k:
+//   warp 0      TMA: X (BN rows, kTerms times for FP32) into shared memory (128-byte swizzle)
+//   warp 1      MMA issuer (M = 128, N = BN, K = 16, A from TMEM, B from shared memory)
+//   warps 2-9   drain: thread = row of W, half of its BN sums in registers; stores
+//   warps 10-13 decode: thread = row of W; codes go from global memory through registers into
+//               the A operand in TMEM (lane = row, two columns of k a word)
+// One barrier says that a stage is full (the bytes of X and the four decoding warps), one that
+// it is empty: every wait and every commit of the issuing thread costs it about 50 clocks, and
+// with separate rings for both operands and 64 columns a stage it was issue that bound the
+// kernel (1550 clocks per 64 columns against 256 of MMA; 549 us for 2048 rows at 11008x4096).
+// The A operand never touches shared memory, so the MMA reads only X there.  The codes' pair
+// order along k ((0,4) (1,5) (2,6) (3,7) of every 8) is that of the columns of X.
+// Every mbarrier wait is bounded; a tile whose wait ran out is stored as NaN.
+#include "gemm_tc.cuh"
+#include "tc_ptx.cuh"
+#include "w4.cuh"
+
+#include <algorithm>
+
+namespace nq {
+namespace w4 {
+
+using namespace tc;
+
+constexpr int kDrainWarps = 8;                   // two to a quarter of the tile's rows, half the columns each
+constexpr int kTcThreads = 32 * (2 + kDrainWarps + 4);
+constexpr int kRing = 4;                         // stages
+constexpr int kStageK = 128;                     // columns of k of a stage
+constexpr int kStageA = kStageK / 2;             // TMEM columns of a stage of the A operand
+constexpr int kSplitUnit = kUnit / kStageK;      // stages of the least part of a split k axis
+
+struct TcArgs {
+    Mat M;
+    int m, B;
+    int stages, parts, part_stages;              // stages of k; parts of the k axis; stages of a part
+    int ntiles, units;                           // tiles of X; (row tile, tile of X, part) units
+    float *out;                                  // [parts][B][m]
+    float out_scale;
+};
+struct TcMaps {
+    CUtensorMap x[kTerms];
+};
+
+// 32 words a lane into TMEM.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,"
+        "%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+        "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// 16 or 32 columns of a lane's TMEM row, asynchronously.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr));
+}
+// The registers may be read from here on.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+// The registers may be read from here on.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// D (TMEM) += A (TMEM) B (shared memory).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// acc (two columns) += s v.
+__device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t v1) {
+    uint64_t a = *reinterpret_cast<uint64_t *>(&acc), v, ss;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(v), "l"(ss));
+    acc = *reinterpret_cast<float2 *>(&a);
+}
+
+// One lane waits, all lanes of the warp learn the outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane) {
+    int ok = 0;
+    if (lane == 0) ok = mbar_wait(bar, parity, nullptr) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
+template <int BN, int T>
+constexpr int tc_smem() { return kRing * T * BN * kStageK * 2 + 1024 + 256; }
+
+// GS: MMA steps (16 columns of k) of a group.
+template <int BN, int T, int GS>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    w4_tc_kernel(const __grid_constant__ TcMaps maps, const TcArgs a) {
+    constexpr int HALF = BN * BK * 2;            // bytes of 64 columns of BN rows of X
+    constexpr int STAGE = T * 2 * HALF;
+    constexpr int GROUP = 16 * GS, GROUPS = kStageK / GROUP;
+    constexpr uint32_t TMEM_COLS = 512;          // two accumulators of BN columns, the A ring
+    static_assert(2 * BN + kRing * kStageA <= 512, "tensor memory");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing * STAGE);
+    uint64_t *empty = full + kRing, *d_full = empty + kRing, *d_empty = d_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 5), mbar_init(&empty[s], 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&d_full[s], 1), mbar_init(&d_empty[s], kDrainWarps);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)),
+                     "r"(TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot, tmem_a = tmem + 2 * BN;
+
+    // unit u: part u % parts of tile u / parts; its stages of k
+    auto stages_of = [&](int unit, int &k0, int &k1) {
+        k0 = unit % a.parts * a.part_stages;
+        k1 = min(a.stages, k0 + a.part_stages);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+                int k0, k1;
+                stages_of(unit, k0, k1);
+                const int n0 = unit / a.parts % a.ntiles * BN;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int s = it % kRing;
+                    if (it >= kRing && !mbar_wait(&empty[s], (it / kRing - 1) & 1, nullptr)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(&full[s], STAGE);
+#pragma unroll
+                    for (int t = 0; t < T; ++t)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_2d(smem + s * STAGE + (2 * t + h) * HALF, &maps.x[t],
+                                        k * kStageK + h * BK, n0, &full[s]);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = instr_desc_bf16(BM, BN);
+            const uint64_t desc0 = smem_desc_sw128(smem);
+            uint32_t it = 0, grp = 0;
+            bool ok = true;
+            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+                int k0, k1;
+                stages_of(unit, k0, k1);
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const uint32_t s = it % kRing;
+                    if (!mbar_wait(&full[s], it / kRing & 1, nullptr)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t desc = desc0 + s * (STAGE / 16);
+                    const uint32_t at = tmem_a + s * kStageA;
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g, ++grp) {
+                        const uint32_t d = tmem + (grp & 1) * BN;
+                        if (grp >= 2) ok = ok && mbar_wait(&d_empty[grp & 1], (grp / 2 - 1) & 1, nullptr);
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < GS; ++i) {
+                            const int step = g * GS + i;     // 16 columns of k of the stage
+#pragma unroll
+                            for (int t = 0; t < T; ++t)
+                                mma_bf16_ts(d, at + 8 * step,
+                                            desc + ((2 * t + step / 4) * HALF / 16 + step % 4 * 2), idesc,
+                                            i != 0 || t != 0);
+                        }
+                        // the stage's release comes before its last group's: the drain's wait
+                        // for the unit's last group then covers every commit of the unit
+                        if (g == GROUPS - 1) mma_commit(&empty[s]);
+                        mma_commit(&d_full[grp & 1]);
+                    }
+                    if (!ok) break;
+                }
+            }
+        }
+    } else if (warp < 2 + kDrainWarps) {
+        // drain: rows of quarter q, columns c0 .. c0 + COLS - 1
+        constexpr int COLS = BN / 2, LD = COLS < 32 ? COLS : 32;
+        const int q = warp & 3, c0 = (warp - 2) / 4 * COLS;
+        uint32_t grp = 0;
+        bool dead = false;
+        for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+            int k0, k1;
+            stages_of(unit, k0, k1);
+            const int tile = unit / a.parts, n0 = tile % a.ntiles * BN + c0;
+            const int row = tile / a.ntiles * BM + 32 * q + lane;
+            const unsigned short *scales = reinterpret_cast<const unsigned short *>(a.M.s) +
+                                           (int64_t)min(row, a.m - 1) * a.M.ng;
+            const int g1 = k1 * GROUPS;
+            float2 acc[COLS / 2];
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            // scales are asked for a group ahead, as they are (past the last group: any; those
+            // groups' columns are zero)
+            uint32_t s_next = __ldg(scales + k0 * GROUPS);
+            for (int g = k0 * GROUPS; g < g1 && !dead; ++g, ++grp) {
+                const float s = __uint_as_float(s_next << 16);
+                s_next = __ldg(scales + min(g + 1, a.M.ng - 1));
+                if (!warp_wait(&d_full[grp & 1], grp / 2 & 1, lane)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = tmem + (grp & 1) * BN + c0 + ((uint32_t)(32 * q) << 16);
+                uint32_t v[COLS / LD][LD];
+#pragma unroll
+                for (int c = 0; c < COLS / LD; ++c) tmem_ld(base + c * LD, v[c]);
+#pragma unroll
+                for (int c = 0; c < COLS / LD; ++c) tmem_ld_wait(v[c]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&d_empty[grp & 1]);
+                // (the accumulator is free for the next group but one while its sums are taken)
+#pragma unroll
+                for (int c = 0; c < COLS / LD; ++c)
+#pragma unroll
+                    for (int j = 0; j < LD; j += 2) fma2(acc[(c * LD + j) / 2], s, v[c][j], v[c][j + 1]);
+            }
+            if (row < a.m) {
+                float *dst = a.out + ((int64_t)(unit % a.parts) * a.B + n0) * a.m + row;
+                const float f = dead ? __int_as_float(0x7fc00000) : a.out_scale;
+#pragma unroll
+                for (int j = 0; j < COLS; ++j)
+                    if (n0 + j < a.B) dst[(int64_t)j * a.m] = f * (j & 1 ? acc[j / 2].y : acc[j / 2].x);
+            }
+        }
+    } else {
+        // decode
+        const int q = warp & 3;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            int k0, k1;
+            stages_of(unit, k0, k1);
+            const int row = min(unit / a.parts / a.ntiles * BM + 32 * q + lane, a.m - 1);
+            const uint32_t *src = a.M.q + (int64_t)row * a.M.ld;
+            const uint8_t *zeros = a.M.z + (int64_t)row * a.M.ng;
+            auto load = [&](int k, uint4 (&w)[4]) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    w[c] = k < k1 && k * 16 + 4 * c < a.M.ld
+                               ? __ldg(reinterpret_cast<const uint4 *>(src + k * 16 + 4 * c))
+                               : make_uint4(0, 0, 0, 0);
+            };
+            uint4 w[2][4];
+            load(k0, w[0]);
+            load(k0 + 1, w[1]);
+            for (int k = k0; k < k1 && ok; k += 2) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (k + i >= k1) break;
+                    uint32_t zv[GROUPS];
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g)
+                        zv[g] = a.M.z ? __ldg(zeros + min((k + i) * GROUPS + g, a.M.ng - 1)) : 8u;
+                    const uint32_t s = it % kRing;
+                    if (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[32];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 v = w[i][2 * h + c / 4];
+                            const uint32_t x = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
+                            const ZeroPoint z = zero_point(zv[(8 * h + c) * 8 / GROUP] & 15u);
+                            r[4 * c] = code_pair0(x, z);
+                            r[4 * c + 1] = code_pair1(x, z);
+                            r[4 * c + 2] = code_pair0(x >> 8, z);
+                            r[4 * c + 3] = code_pair1(x >> 8, z);
+                        }
+                        tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), r);
+                    }
+                    load(k + i + 2, w[i]);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
+                    ++it;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(TMEM_COLS)
+                     : "memory");
+    }
+}
+
+// Y = sum over the parts, in their order.
+__global__ void __launch_bounds__(256)
+    w4_sum_parts_kernel(const float *__restrict__ part, int parts, int64_t count,
+                        float *__restrict__ Y) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < count;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        float v = 0.f;
+        for (int p = 0; p < parts; ++p) v += part[p * count + i];
+        Y[i] = v;
+    }
+}
+
+TcPlan tc_plan(int64_t m, int64_t n, int terms, int64_t B) {
+    TcPlan p;
+    p.BN = B <= 32 ? 32 : B <= 64 || terms > 1 ? 64 : 128;
+    const int64_t tiles = ceil_div(m, BM) * ceil_div(B, p.BN), axis = ceil_div(n, kUnit);
+    int64_t parts = tiles >= kNumSMsB200 ? 1 : kNumSMsB200 / tiles;
+    if (parts > axis / 2) parts = axis / 2;      // at least two units of k a part
+    if (parts < 1) parts = 1;
+    p.part_units = (int)ceil_div(axis, parts);
+    p.parts = (int)ceil_div(axis, p.part_units); // none of them empty
+    p.partial_bytes = p.parts > 1 ? (size_t)p.parts * B * m * 4 : 0;
+    return p;
+}
+
+template <int BN, int T, int GS>
+static cudaError_t tc_launch_g(const TcMaps &maps, const TcArgs &a, cudaStream_t st) {
+    auto kern = w4_tc_kernel<BN, T, GS>;
+    constexpr int smem = tc_smem<BN, T>();
+    static_assert(smem <= 227 * 1024, "shared memory of the ring of X");
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = ensure_smem_limit((const void *)kern, smem, configured);
+    if (e != cudaSuccess) return e;
+    const int sms = device_sm_count();
+    kern<<<(unsigned)(a.units < sms ? a.units : sms), kTcThreads, smem, st>>>(maps, a);
+    count_launch();
+    return cudaGetLastError();
+}
+
+template <int BN, int T>
+static cudaError_t tc_launch(const TcMaps &maps, const TcArgs &a, int group, cudaStream_t st) {
+    return group == 32   ? tc_launch_g<BN, T, 2>(maps, a, st)
+           : group == 64 ? tc_launch_g<BN, T, 4>(maps, a, st)
+                         : tc_launch_g<BN, T, 8>(maps, a, st);
+}
+
+cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *xw, int terms, int64_t B,
+                      float *Y, float *partial, cudaStream_t st) {
+    const TcPlan p = tc_plan(m, M.n, terms, B);
+    const int64_t ldx = padded(M.n);
+    TcMaps maps;
+    for (int t = 0; t < terms; ++t)
+        if (!make_map_bf16(&maps.x[t], xw + t * ldx, B, ldx, terms * ldx, p.BN))
+            return cudaErrorInvalidValue;
+    TcArgs a;
+    a.M = M;
+    a.m = (int)m, a.B = (int)B;
+    a.stages = (int)ceil_div(M.n, kStageK);
+    a.parts = p.parts;
+    a.part_stages = p.part_units * kSplitUnit;
+    a.ntiles = (int)ceil_div(B, p.BN);
+    a.units = (int)ceil_div(m, BM) * a.ntiles * p.parts;
+    a.out = p.parts > 1 ? partial : Y;
+    a.out_scale = kCodeUnit;
+    cudaError_t e;
+    if (terms == 1)
+        e = p.BN == 32    ? tc_launch<32, 1>(maps, a, group, st)
+            : p.BN == 64  ? tc_launch<64, 1>(maps, a, group, st)
+                          : tc_launch<128, 1>(maps, a, group, st);
+    else
+        e = p.BN == 32 ? tc_launch<32, kTerms>(maps, a, group, st)
+                       : tc_launch<64, kTerms>(maps, a, group, st);
+    if (e != cudaSuccess || p.parts == 1) return e;
+    const int64_t count = B * m;
+    w4_sum_parts_kernel<<<(unsigned)std::min<int64_t>(ceil_div(count, 256), 4 * kNumSMsB200), 256, 0, st>>>(
+        partial, p.parts, count, Y);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace w4
+}  // namespace nq
