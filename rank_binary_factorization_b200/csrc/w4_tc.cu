@@ -95,6 +95,13 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t tmem_d, uint32_t tmem_a, ui
         "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate));
 }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // acc (two columns) += s v.
 __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t v1) {
     uint64_t a = *reinterpret_cast<uint64_t *>(&acc), v, ss;
@@ -179,27 +186,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = instr_desc_bf16(BM, BN);
-            const uint64_t desc0 = smem_desc_sw128(smem);
-            uint32_t it = 0, grp = 0;
-            bool ok = true;
-            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-                int k0, k1;
-                stages_of(unit, k0, k1);
-                for (int k = k0; k < k1; ++k, ++it) {
-                    const uint32_t s = it % kRing;
-                    if (!mbar_wait(&full[s], it / kRing & 1, nullptr)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint64_t desc = desc0 + s * (STAGE / 16);
-                    const uint32_t at = tmem_a + s * kStageA;
+        // the whole warp walks the loop, so that the operands' addresses are uniform; one lane
+        // issues
+        constexpr uint32_t idesc = instr_desc_bf16(BM, BN);
+        const bool leader = elect_one();
+        const uint64_t desc0 = smem_desc_sw128(smem);
+        uint32_t it = 0, grp = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            int k0, k1;
+            stages_of(unit, k0, k1);
+            for (int k = k0; k < k1 && ok; ++k, ++it) {
+                const uint32_t s = it % kRing;
+                ok = mbar_wait(&full[s], it / kRing & 1, nullptr);
+                if (!ok) break;
+                const uint64_t desc = desc0 + s * (STAGE / 16);
+                const uint32_t at = tmem_a + s * kStageA;
 #pragma unroll
-                    for (int g = 0; g < GROUPS; ++g, ++grp) {
-                        const uint32_t d = tmem + (grp & 1) * BN;
-                        if (grp >= 2) ok = ok && mbar_wait(&d_empty[grp & 1], (grp / 2 - 1) & 1, nullptr);
-                        tc_fence_after();
+                for (int g = 0; g < GROUPS; ++g, ++grp) {
+                    const uint32_t d = tmem + (grp & 1) * BN;
+                    if (grp >= 2) ok = mbar_wait(&d_empty[grp & 1], (grp / 2 - 1) & 1, nullptr) && ok;
+                    tc_fence_after();
+                    if (leader) {
 #pragma unroll
                         for (int i = 0; i < GS; ++i) {
                             const int step = g * GS + i;     // 16 columns of k of the stage
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (g == GROUPS - 1) mma_commit(&empty[s]);
                         mma_commit(&d_full[grp & 1]);
                     }
-                    if (!ok) break;
+                    __syncwarp();
                 }
             }
         }
@@ -298,6 +306,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int g = 0; g < GROUPS; ++g)
                         zv[g] = a.M.z ? __ldg(zeros + min((k + i) * GROUPS + g, a.M.ng - 1)) : 8u;
+                    uint32_t r[2][32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 v = w[i][2 * h + c / 4];
+                            const uint32_t x = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
+                            const ZeroPoint z = zero_point(zv[(8 * h + c) * 8 / GROUP] & 15u);
+                            r[h][4 * c] = code_pair0(x, z);
+                            r[h][4 * c + 1] = code_pair1(x, z);
+                            r[h][4 * c + 2] = code_pair0(x >> 8, z);
+                            r[h][4 * c + 3] = code_pair1(x >> 8, z);
+                        }
+                    load(k + i + 2, w[i]);
                     const uint32_t s = it % kRing;
                     if (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane)) {
                         ok = false;
@@ -305,21 +327,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tc_fence_after();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t r[32];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 v = w[i][2 * h + c / 4];
-                            const uint32_t x = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
-                            const ZeroPoint z = zero_point(zv[(8 * h + c) * 8 / GROUP] & 15u);
-                            r[4 * c] = code_pair0(x, z);
-                            r[4 * c + 1] = code_pair1(x, z);
-                            r[4 * c + 2] = code_pair0(x >> 8, z);
-                            r[4 * c + 3] = code_pair1(x >> 8, z);
-                        }
-                        tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), r);
-                    }
-                    load(k + i + 2, w[i]);
+                    for (int h = 0; h < 2; ++h)
+                        tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), r[h]);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
