@@ -1441,18 +1441,19 @@ nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t
 
 namespace {
 struct MoeLayout {
-    size_t ids = 0, weights = 0, xw = 0, h = 0, total = 0;
-    MoeLayout(int64_t B, int64_t d, int64_t f, int top_k, int dt) {
+    size_t bar = 0, logits = 0, xw = 0, h = 0, part = 0, total = 0;
+    MoeLayout(int64_t B, int64_t d, int64_t f, int E, int top_k, int dt) {
         size_t off = 0;
         auto take = [&](size_t bytes) {
             const size_t o = off;
             off = align_up(off + bytes);
             return o;
         };
-        ids = take((size_t)B * top_k * 4);
-        weights = take((size_t)B * top_k * 4);
+        bar = take(2 * sizeof(unsigned int));
+        logits = take((size_t)B * E * 8);
         xw = take((size_t)B * (dt == NQ_BF16 ? 1 : w4::kTerms) * w4::padded(d) * 2);
         h = take((size_t)B * top_k * w4::kTerms * w4::padded(f) * 2);
+        part = take((size_t)B * top_k * d * 4);
         total = off;
     }
 };
@@ -1467,7 +1468,7 @@ bool moe_sizes_ok(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k) {
 size_t nq_moe_workspace_size(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k,
                              nq_dtype dt) {
     if (!moe_sizes_ok(B, d, f, E, top_k) || !dtype_ok(dt)) return 0;
-    return MoeLayout(B, d, f, top_k, dt).total;
+    return MoeLayout(B, d, f, E, top_k, dt).total;
 }
 
 nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void *router, int32_t E,
@@ -1482,7 +1483,7 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
         (ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4)) || renormalise < 0 ||
         renormalise > 1)
         return NQ_ERR_INVALID_ARG;
-    const MoeLayout L(B, d, f, top_k, dt);
+    const MoeLayout L(B, d, f, E, top_k, dt);
     nq_status st = check_ws(ws, ws_bytes, L.total);
     if (st) return st;
     if ((st = check_device())) return st;
@@ -1496,10 +1497,13 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     a.down = w4_mat(down, down_scales, down_zeros, f, group);
     a.group = group;
     a.Y = Y;
-    a.ids = ids ? ids : at<int32_t>(ws, L.ids);
-    a.weights = weights ? weights : at<float>(ws, L.weights);
-    a.xw = at<__nv_bfloat16>(ws, L.xw);
+    a.ids = ids;
+    a.weights = weights;
+    a.bar = at<unsigned int>(ws, L.bar);
+    a.logits = at<double>(ws, L.logits);
+    a.xw = at<uint4>(ws, L.xw);
     a.h = at<__nv_bfloat16>(ws, L.h);
+    a.part = at<float>(ws, L.part);
     ProfScope ps(NQ_K_MOE, cs(stream));
     NQ_CK(w4::moe(a, cs(stream)));
     return NQ_OK;

@@ -7,39 +7,62 @@
 namespace nq {
 namespace w4 {
 
-constexpr int kMoeWarps = 8;
 constexpr int kMoeMaxPairs = NQ_MOE_MAX_TOKENS * NQ_MOE_MAX_TOP_K;
+constexpr int kRouterTokens = 8;       // tokens of a CTA of the router
 
-// ---- router -------------------------------------------------------------------------
-// One CTA per token.  The logits are summed in FP64: which experts are chosen must not
-// depend on the order of the sum.
+// ---- router logits, columns of X --------------------------------------------------------
+// CTA: one expert, up to 8 tokens; the sums are in FP64, so that which experts are chosen does
+// not depend on their order.  The CTAs together also write X's columns in word order and clear
+// the arrival counts of the kernel that follows.
 template <typename T>
-__global__ void __launch_bounds__(32 * kMoeWarps) moe_router_kernel(const MoeArgs a) {
-    __shared__ double logit[NQ_MOE_MAX_EXPERTS];
+__global__ void __launch_bounds__(256) moe_logits_kernel(const MoeArgs a) {
+    __shared__ double red[8][kRouterTokens];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.x;
-    const T *x = static_cast<const T *>(a.X) + (int64_t)b * a.d;
-    for (int e = warp; e < a.E; e += kMoeWarps) {
-        const T *r = static_cast<const T *>(a.router) + (int64_t)e * a.d;
-        double v = 0.0;
-        for (int k = lane; k < a.d; k += 32) v += (double)(float)x[k] * (double)(float)r[k];
-        v = warp_sum(v);
-        if (lane == 0) logit[e] = v;
+    const int e = blockIdx.x, b0 = blockIdx.y * kRouterTokens;
+    const int nb = min(kRouterTokens, a.B - b0);
+    const T *X = static_cast<const T *>(a.X);
+    if (e == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.bar[threadIdx.x] = 0;
+    const T *r = static_cast<const T *>(a.router) + (int64_t)e * a.d;
+    double acc[kRouterTokens] = {};
+    for (int k = threadIdx.x; k < a.d; k += 256) {
+        const double rv = (double)(float)r[k];
+#pragma unroll
+        for (int b = 0; b < kRouterTokens; ++b)
+            if (b < nb) acc[b] += rv * (double)(float)X[(int64_t)(b0 + b) * a.d + k];
+    }
+#pragma unroll
+    for (int b = 0; b < kRouterTokens; ++b) {
+        if (b >= nb) break;
+        const double v = warp_sum(acc[b]);
+        if (lane == 0) red[warp][b] = v;
     }
     const int words = (int)(padded(a.d) / 8);
-    for (int wd = threadIdx.x; wd < words; wd += blockDim.x) {
-        uint4 *dst = reinterpret_cast<uint4 *>(a.xw);
+    const int ctas = gridDim.x * gridDim.y, cta = blockIdx.y * gridDim.x + blockIdx.x;
+    for (int o = cta * 256 + threadIdx.x; o < a.B * words; o += ctas * 256) {
+        const int b = o / words, wd = o % words;
         if constexpr (sizeof(T) == 2) {
-            dst[(int64_t)b * words + wd] = x_word(x, wd * 8, a.d);
+            a.xw[o] = x_word(X + (int64_t)b * a.d, wd * 8, a.d);
         } else {
             uint4 w[kTerms];
-            x_words(x, wd * 8, a.d, w);
+            x_words(X + (int64_t)b * a.d, wd * 8, a.d, w);
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) dst[((int64_t)b * kTerms + t) * words + wd] = w[t];
+            for (int t = 0; t < kTerms; ++t) a.xw[((int64_t)b * kTerms + t) * words + wd] = w[t];
         }
     }
     __syncthreads();
-    if (warp != 0) return;
+    if (threadIdx.x < nb) {
+        double v = 0.0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) v += red[w][threadIdx.x];
+        a.logits[(int64_t)(b0 + threadIdx.x) * a.E + e] = v;
+    }
+}
+
+// ---- choice of experts --------------------------------------------------------------------
+// One warp, one token: the top_k largest logits (ties: the lowest expert) and their weights.
+__device__ void choose(const MoeArgs &a, int b, short *ids, float *weights) {
+    const int lane = threadIdx.x & 31;
+    const double *logit = a.logits + (int64_t)b * a.E;
     // lane l looks after experts l, l + 32, ...; the winner of each round leaves
     unsigned int gone = 0;
     double top = 0.0, sum = 0.0;
@@ -48,8 +71,11 @@ __global__ void __launch_bounds__(32 * kMoeWarps) moe_router_kernel(const MoeArg
     for (int j = 0; j < a.top_k; ++j) {
         double best = 0.0;
         int at = -1;
-        for (int e = lane, i = 0; e < a.E; e += 32, ++i)
-            if (!(gone >> i & 1) && (at < 0 || logit[e] > best)) best = logit[e], at = e;
+        for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
+            if (gone >> i & 1) continue;
+            const double v = logit[e];
+            if (at < 0 || v > best) best = v, at = e;
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const double ob = __shfl_xor_sync(0xffffffffu, best, o);
@@ -69,35 +95,45 @@ __global__ void __launch_bounds__(32 * kMoeWarps) moe_router_kernel(const MoeArg
         sum = warp_sum(sum);
     }
     if (lane < a.top_k) {
-        a.ids[b * a.top_k + lane] = chosen;
-        a.weights[b * a.top_k + lane] = (float)(exp(mine - top) / sum);
+        ids[b * a.top_k + lane] = (short)chosen;
+        weights[b * a.top_k + lane] = (float)(exp(mine - top) / sum);
     }
 }
 
 // ---- (token, expert) pairs by expert -------------------------------------------------
 // Experts that some token chose, in ascending order, and their pairs (pair = token top_k +
-// choice).  The order of an expert's pairs does not reach any result: every pair is a
-// column of its own.
+// choice) by token: the same lists in every CTA.
 struct Lists {
-    int count[NQ_MOE_MAX_EXPERTS];
     short expert[NQ_MOE_MAX_EXPERTS];        // active expert a
     short first[NQ_MOE_MAX_EXPERTS + 1];     // its first place in pairs[]
-    short at[NQ_MOE_MAX_EXPERTS];            // expert -> a
     short pairs[kMoeMaxPairs];
-    int active;
+    float weights[kMoeMaxPairs];
+    int active, chunks;
+    union {
+        short at[NQ_MOE_MAX_EXPERTS];        // expert -> a, while the lists are built
+        short chunk_first[kMoeMaxPairs];     // later: chunks of an expert's pairs, as many as one
+    };                                       // job takes
+    union {
+        short ids[kMoeMaxPairs];             // chosen experts, pair by pair; likewise
+        short chunk_active[kMoeMaxPairs];
+    };
 };
 
-__device__ void build_lists(Lists &L, const int32_t *ids, int npairs, int E) {
-    for (int e = threadIdx.x; e < E; e += blockDim.x) L.count[e] = 0;
+// users: scratch, two words of tokens an expert.
+__device__ void build_lists(Lists &L, unsigned int (*users)[2], int npairs, int top_k, int E) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) users[e][0] = users[e][1] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < npairs; p += blockDim.x) atomicAdd(&L.count[ids[p]], 1);
+    for (int p = threadIdx.x; p < npairs; p += blockDim.x) {
+        const int b = p / top_k;
+        atomicOr(&users[L.ids[p]][b >> 5], 1u << (b & 31));
+    }
     __syncthreads();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         int na = 0, np = 0;
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
-            const int c = e < E ? L.count[e] : 0;
+            const int c = e < E ? __popc(users[e][0]) + __popc(users[e][1]) : 0;
             const unsigned int used = __ballot_sync(0xffffffffu, c > 0);
             int incl = c;
 #pragma unroll
@@ -110,7 +146,6 @@ __device__ void build_lists(Lists &L, const int32_t *ids, int npairs, int E) {
                 L.expert[i] = (short)e;
                 L.first[i] = (short)(np + incl - c);
                 L.at[e] = (short)i;
-                L.count[e] = 0;
             }
             na += __popc(used);
             np += __shfl_sync(0xffffffffu, incl, 31);
@@ -119,45 +154,118 @@ __device__ void build_lists(Lists &L, const int32_t *ids, int npairs, int E) {
     }
     __syncthreads();
     for (int p = threadIdx.x; p < npairs; p += blockDim.x) {
-        const int e = ids[p];
-        L.pairs[L.first[L.at[e]] + atomicAdd(&L.count[e], 1)] = (short)p;
+        const int e = L.ids[p], b = p / top_k;
+        const unsigned int below = (1u << (b & 31)) - 1;
+        const int rank = b < 32 ? __popc(users[e][0] & below)
+                                : __popc(users[e][0]) + __popc(users[e][1] & below);
+        L.pairs[L.first[L.at[e]] + rank] = (short)p;
     }
     __syncthreads();
 }
 
-// ---- gate and up projections, activation ----------------------------------------------
-// Job: 16 of an expert's f rows, gate and up side by side (two row tiles), against up to 8
-// columns of its pairs.  h leaves in kTerms BF16 columns.  A CTA does one expert's jobs.
-struct GateUpProb {
+// Chunks of up to ``per`` pairs, expert by expert (all threads).
+__device__ void build_chunks(Lists &L, int per) {
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        int n = 0;
+        for (int i0 = 0; i0 < L.active; i0 += 32) {
+            const int i = i0 + lane;
+            const int p0 = i < L.active ? L.first[i] : 0, p1 = i < L.active ? L.first[i + 1] : 0;
+            const int c = (p1 - p0 + per - 1) / per;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            for (int k = 0; k < c; ++k) {
+                L.chunk_active[n + incl - c + k] = (short)i;
+                L.chunk_first[n + incl - c + k] = (short)(p0 + k * per);
+            }
+            n += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) L.chunks = n;
+    }
+    __syncthreads();
+}
+
+// ---- the experts ----------------------------------------------------------------------------
+// Arrival of all CTAs (launched together): bounded.
+__device__ __forceinline__ void arrive(unsigned int *bar) {
+    __syncthreads();
+    if (threadIdx.x == 0) release_add(bar, 1);
+}
+__device__ __forceinline__ bool all_arrived(unsigned int *bar) {
+    bool ok = true;
+    if (threadIdx.x == 0) ok = wait_geq(bar, gridDim.x, kGridSpinLimit);
+    return __syncthreads_and(ok);
+}
+
+// The jobs of both projections: job k of a CTA is number blockIdx.x + k gridDim.x of (chunk of an
+// expert's pairs, block of its rows).
+struct ExpertJobs {
     int jobs, WK;
     static constexpr uint32_t half_stride = 0;
     const MoeArgs &a;
     const Lists &L;
-    Red<2, 1> *red;
-    int terms, per, e, first, pairs, r0, p0 = 0, np = 0;
-    int64_t ldx, ldh;
+    int terms, per, lrows, blocks;         // columns of a pair, pairs of a chunk, log2 rows of a block
+    int64_t ld;                            // 16-byte words of a column
+    int p0 = 0, np = 0, r0 = 0;            // the running job
 
-    __device__ __forceinline__ int first_row(int, int wr, int i) const {
-        return (e * 2 + i) * a.f + r0 + wr * 16;
+    __device__ ExpertJobs(const MoeArgs &a_, const Lists &L_, int n, int rows, int mt_rows, int terms_,
+                          int per_)
+        : WK(k_ranges(n)), a(a_), L(L_), terms(terms_), per(per_) {
+        lrows = 31 - __clz(mt_rows * (kWarps / WK));
+        blocks = (rows + (1 << lrows) - 1) >> lrows;
+        ld = padded(n) / 8;
+        const int all = L.chunks * blocks;
+        jobs = ((int)blockIdx.x < all) ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
     }
-    __device__ __forceinline__ int last_row(int, int i) const { return (e * 2 + i + 1) * a.f - 1; }
-    __device__ __forceinline__ void ready() const {}
+    __device__ __forceinline__ int nth(int job) const { return blockIdx.x + job * gridDim.x; }
+    __device__ __forceinline__ int expert(int n) const { return L.expert[L.chunk_active[n / blocks]]; }
     __device__ __forceinline__ void begin(int job) {
-        p0 = first + job * per;
-        np = min(per, first + pairs - p0);
+        const int n = nth(job), c = n / blocks;
+        r0 = (n - c * blocks) << lrows;
+        p0 = L.chunk_first[c];
+        np = min(per, L.first[L.chunk_active[c] + 1] - p0);
     }
-    __device__ __forceinline__ const char *col(int) const {
-        const int c = min(((int)threadIdx.x & 31) >> 2, np * terms - 1);
-        return reinterpret_cast<const char *>(
-            a.xw + ((int64_t)(L.pairs[p0 + c / terms] / a.top_k) * terms + c % terms) * ldx);
+    __device__ __forceinline__ int tiles(int) const { return (np * terms + 7) / 8; }
+    // the lane's column of n-tile j as (pair, term)
+    __device__ __forceinline__ void column(int j, int &pair, int &term) const {
+        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), np * terms - 1);
+        pair = L.pairs[p0 + c / terms];
+        term = c % terms;
     }
-    __device__ __forceinline__ void end(int job, const float (&acc)[2][1][4]) {
-        Red<2, 1> &R = red[job & 1];
+};
+
+// Gate and up projections: 16 rows of each side by side (two row tiles of a warp).  h leaves in
+// kTerms BF16 columns, its padding past f as zeros.
+template <int NT>
+struct GateUpProb : ExpertJobs {
+    Red<2, NT> *red;
+    int64_t ldh;
+    __device__ GateUpProb(const MoeArgs &a, const Lists &L, int terms, int per, Red<2, NT> *red_)
+        : ExpertJobs(a, L, a.d, (int)padded(a.f), 16, terms, per), red(red_), ldh(padded(a.f)) {}
+    __device__ __forceinline__ int first_row(int job, int wr, int i) const {
+        const int n = nth(job);
+        return (expert(n) * 2 + i) * a.f + (n % blocks << lrows) + wr * 16;
+    }
+    __device__ __forceinline__ int last_row(int job, int i) const {
+        return (expert(nth(job)) * 2 + i + 1) * a.f - 1;
+    }
+    __device__ __forceinline__ void ready() const {}
+    __device__ __forceinline__ const char *col(int j) const {
+        int pair, term;
+        column(j, pair, term);
+        return reinterpret_cast<const char *>(a.xw + ((int64_t)(pair / a.top_k) * terms + term) * ld);
+    }
+    __device__ __forceinline__ void end(int job, const float (&acc)[2][NT][4]) {
+        Red<2, NT> &R = red[job & 1];
         R.put(acc);
         __syncthreads();
-        const int rows = 16 * (kWarps / WK);
-        for (int o = threadIdx.x; o < rows * np; o += 32 * kWarps) {
-            const int r = o % rows, p = o / rows, k = r0 + r;
+        for (int o = threadIdx.x; o < np << lrows; o += 32 * kWarps) {
+            const int r = o & ((1 << lrows) - 1), p = o >> lrows, k = r0 + r;
             if (k >= ldh) continue;
             const float g = R.sum(r / 16, WK, r % 16, p * terms, terms),
                         u = R.sum(r / 16, WK, 16 + r % 16, p * terms, terms);
@@ -170,139 +278,149 @@ struct GateUpProb {
     }
 };
 
-template <int VW, bool Z>
-__global__ void __launch_bounds__(32 * kWarps, 2) moe_gate_up_kernel(const MoeArgs a) {
-    extern __shared__ __align__(1024) char sm[];
-    Red<2, 1> *red = reinterpret_cast<Red<2, 1> *>(sm + ring_bytes<2>());
-    Lists &L = *reinterpret_cast<Lists *>(red + 2);
-    build_lists(L, a.ids, a.B * a.top_k, a.E);
-    if ((int)blockIdx.y >= L.active) return;
-    const int WK = k_ranges(a.d);
-    GateUpProb P{0, WK, a, L, red};
-    P.terms = a.x_bf16 ? 1 : kTerms;
-    P.per = 8 / P.terms;
-    P.e = L.expert[blockIdx.y];
-    P.first = L.first[blockIdx.y];
-    P.pairs = L.first[blockIdx.y + 1] - P.first;
-    P.r0 = blockIdx.x * 16 * (kWarps / WK);
-    P.jobs = (P.pairs + P.per - 1) / P.per;
-    P.ldx = padded(a.d);
-    P.ldh = padded(a.f);
-    run_products<VW, Z, false, 2, 1>(P, a.gate_up, a.svec_gate_up, WK, sm);
-}
-
-// ---- down projection and combination ---------------------------------------------------
-// CTA: one block of rows of d, all active experts in ascending order (jobs: chunks of an
-// expert's pairs); y is summed in shared memory.
-struct DownProb {
-    int jobs, WK;
-    static constexpr uint32_t half_stride = 0;
-    const MoeArgs &a;
-    const Lists &L;
-    Red<1, 1> *red;
-    float *y;                              // [B][rows]
-    const short *job_expert, *job_pair;    // active expert and first pair of a job
-    int r0;
-    int64_t ldh;
-    int p0 = 0, np = 0;
-
+// Down projection, pair by pair.
+template <int NT>
+struct DownProb : ExpertJobs {
+    Red<1, NT> *red;
+    bool ok = true;                        // all of h was there
+    __device__ DownProb(const MoeArgs &a, const Lists &L, int per, Red<1, NT> *red_)
+        : ExpertJobs(a, L, a.f, a.d, 16, kTerms, per), red(red_) {}
     __device__ __forceinline__ int first_row(int job, int wr, int) const {
-        return L.expert[job_expert[job]] * a.d + r0 + wr * 16;
+        const int n = nth(job);
+        return expert(n) * a.d + (n % blocks << lrows) + wr * 16;
     }
     __device__ __forceinline__ int last_row(int job, int) const {
-        return (L.expert[job_expert[job]] + 1) * a.d - 1;
+        return (expert(nth(job)) + 1) * a.d - 1;
     }
-    __device__ __forceinline__ void ready() const {}
-    __device__ __forceinline__ void begin(int job) {
-        p0 = job_pair[job];
-        np = min(8 / kTerms, L.first[job_expert[job] + 1] - p0);
+    // the first copies of the weights are under way; h is complete when all CTAs have arrived
+    __device__ __forceinline__ void ready() { ok = all_arrived(a.bar); }
+    __device__ __forceinline__ const char *col(int j) const {
+        int pair, term;
+        column(j, pair, term);
+        return reinterpret_cast<const char *>(reinterpret_cast<const uint4 *>(a.h) +
+                                              ((int64_t)pair * kTerms + term) * ld);
     }
-    __device__ __forceinline__ const char *col(int) const {
-        const int c = min(((int)threadIdx.x & 31) >> 2, np * kTerms - 1);
-        return reinterpret_cast<const char *>(
-            a.h + ((int64_t)L.pairs[p0 + c / kTerms] * kTerms + c % kTerms) * ldh);
-    }
-    __device__ __forceinline__ void end(int job, const float (&acc)[1][1][4]) {
-        Red<1, 1> &R = red[job & 1];
+    __device__ __forceinline__ void end(int job, const float (&acc)[1][NT][4]) {
+        Red<1, NT> &R = red[job & 1];
         R.put(acc);
         __syncthreads();
-        // one pair of a token per expert, and a barrier between two jobs: fixed order
-        const int rows = 16 * (kWarps / WK);
-        for (int o = threadIdx.x; o < rows * np; o += 32 * kWarps) {
-            const int r = o % rows, p = o / rows, pair = L.pairs[p0 + p];
-            y[pair / a.top_k * rows + r] +=
-                a.weights[pair] * R.sum(r / 16, WK, r % 16, p * kTerms, kTerms);
+        for (int o = threadIdx.x; o < np << lrows; o += 32 * kWarps) {
+            const int r = o & ((1 << lrows) - 1), p = o >> lrows;
+            if (r0 + r < a.d)
+                a.part[(int64_t)L.pairs[p0 + p] * a.d + r0 + r] =
+                    R.sum(r / 16, WK, r % 16, p * kTerms, kTerms);
         }
     }
 };
 
-template <int VW, bool Z>
-__global__ void __launch_bounds__(32 * kWarps, 2) moe_down_kernel(const MoeArgs a) {
+// All CTAs of the launch are resident together (cooperative launch): choice and lists in every
+// CTA, gate and up jobs, arrival, down jobs, arrival, and y = sum over a token's choices of p times
+// the pair's output, in the order of the choices.
+template <int VW, bool Z, int TERMS>
+__global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeArgs a) {
+    constexpr int NU = TERMS == 1 ? 1 : 2, ND = 2;
     extern __shared__ __align__(1024) char sm[];
-    Red<1, 1> *red = reinterpret_cast<Red<1, 1> *>(sm + ring_bytes<1>());
-    Lists &L = *reinterpret_cast<Lists *>(red + 2);
-    short *job_expert = reinterpret_cast<short *>(&L + 1);
-    short *job_pair = job_expert + kMoeMaxPairs;
-    float *y = reinterpret_cast<float *>(job_pair + kMoeMaxPairs);
-    __shared__ int njobs;
-    const int WK = k_ranges(a.f), rows = 16 * (kWarps / WK);
-    build_lists(L, a.ids, a.B * a.top_k, a.E);
-    for (int o = threadIdx.x; o < rows * a.B; o += blockDim.x) y[o] = 0.f;
-    if (threadIdx.x == 0) {
-        int n = 0;
-        for (int i = 0; i < L.active; ++i)
-            for (int p = L.first[i]; p < L.first[i + 1]; p += 8 / kTerms, ++n)
-                job_expert[n] = (short)i, job_pair[n] = (short)p;
-        njobs = n;
+    void *red = sm + ring_bytes<1>();
+    constexpr size_t kRed = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
+                                                                         : sizeof(Red<1, ND>));
+    Lists &L = *reinterpret_cast<Lists *>(sm + ring_bytes<1>() + kRed);
+    const int pairs = a.B * a.top_k;
+    for (int b = threadIdx.x >> 5; b < a.B; b += kWarps) choose(a, b, L.ids, L.weights);
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int p = threadIdx.x; p < pairs; p += 32 * kWarps) {
+            if (a.ids) a.ids[p] = L.ids[p];
+            if (a.weights) a.weights[p] = L.weights[p];
+        }
+    // (the ring of copies is not in use yet)
+    build_lists(L, reinterpret_cast<unsigned int(*)[2]>(sm), pairs, a.top_k, a.E);
+    build_chunks(L, 8 * NU / TERMS);
+    {
+        GateUpProb<NU> P(a, L, TERMS, 8 * NU / TERMS, static_cast<Red<2, NU> *>(red));
+        if (P.jobs > 0) run_products<VW, Z, false, 2, NU>(P, a.gate_up, a.svec_gate_up, P.WK, sm);
     }
-    __syncthreads();
-    DownProb P{njobs, WK, a, L, red, y, job_expert, job_pair, (int)blockIdx.x * rows, padded(a.f)};
-    run_products<VW, Z, false, 1, 1>(P, a.down, a.svec_down, WK, sm);
-    __syncthreads();
-    for (int o = threadIdx.x; o < rows * a.B; o += blockDim.x)
-        if (P.r0 + o % rows < a.d) a.Y[(int64_t)(o / rows) * a.d + P.r0 + o % rows] = y[o];
+    __threadfence();
+    arrive(a.bar);
+    build_chunks(L, 8 * ND / kTerms);
+    bool ok = true;
+    {
+        DownProb<ND> P(a, L, 8 * ND / kTerms, static_cast<Red<1, ND> *>(red));
+        if (P.jobs > 0) {
+            run_products<VW, Z, false, 1, ND>(P, a.down, a.svec_down, P.WK, sm);
+            ok = P.ok;
+        }
+    }
+    __threadfence();
+    arrive(a.bar + 1);
+    ok = all_arrived(a.bar + 1) && ok;
+    const int64_t count = (int64_t)a.B * a.d;
+    for (int64_t o = (int64_t)blockIdx.x * 32 * kWarps + threadIdx.x; o < count;
+         o += (int64_t)gridDim.x * 32 * kWarps) {
+        const int b = (int)(o / a.d), r = (int)(o % a.d);
+        float y = 0.f;
+        for (int j = 0; j < a.top_k; ++j)
+            y += L.weights[b * a.top_k + j] * __ldcg(a.part + (int64_t)(b * a.top_k + j) * a.d + r);
+        a.Y[o] = ok ? y : __int_as_float(0x7fc00000);       // a wait ran out
+    }
 }
 
-template <class K>
-static cudaError_t moe_launch(K kern, dim3 grid, int smem, const MoeArgs &a, cudaStream_t st,
-                              std::atomic<uint64_t> &configured) {
+template <int VW, bool Z, int TERMS>
+static cudaError_t moe_launch(const MoeArgs &a, cudaStream_t st) {
+    constexpr int NU = TERMS == 1 ? 1 : 2, ND = 2;
+    constexpr size_t red = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
+                                                                        : sizeof(Red<1, ND>));
+    constexpr int smem = ring_bytes<1>() + (int)red + (int)sizeof(Lists);
+    auto kern = moe_experts_kernel<VW, Z, TERMS>;
+    static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit((const void *)kern, smem, configured);
     if (e != cudaSuccess) return e;
-    kern<<<grid, 32 * kWarps, smem, st>>>(a);
+    // CTAs an SM, per device (0: not asked yet)
+    static std::atomic<int> fit[kMaxDevices];
+    const int dev = current_device();
+    if (dev < 0) return cudaErrorInvalidDevice;
+    int n = fit[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, 32 * kWarps, smem);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        fit[dev].store(n, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(n * device_sm_count()));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     count_launch();
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int VW>
 static cudaError_t moe_experts(const MoeArgs &a, cudaStream_t st) {
-    static std::atomic<uint64_t> c0[2], c1[2];
-    const int pairs = a.B * a.top_k;
-    constexpr int s0 = ring_bytes<2>() + 2 * sizeof(Red<2, 1>) + sizeof(Lists);
-    constexpr int s1 = ring_bytes<1>() + 2 * sizeof(Red<1, 1>) + sizeof(Lists) + 4 * kMoeMaxPairs +
-                       NQ_MOE_MAX_TOKENS * 16 * kWarps * 4;
-    const int zu = a.gate_up.z != nullptr, zd = a.down.z != nullptr;
-    const int ru = 16 * (kWarps / k_ranges(a.d)), rd = 16 * (kWarps / k_ranges(a.f));
-    // the columns of h past f are written by the blocks that cover them
-    cudaError_t e = moe_launch(zu ? moe_gate_up_kernel<VW, true> : moe_gate_up_kernel<VW, false>,
-                               dim3((unsigned)ceil_div(padded(a.f), ru),
-                                    (unsigned)(pairs < a.E ? pairs : a.E)),
-                               s0, a, st, c0[zu]);
-    if (e != cudaSuccess) return e;
-    return moe_launch(zd ? moe_down_kernel<VW, true> : moe_down_kernel<VW, false>,
-                      dim3((unsigned)ceil_div(a.d, rd)), s1, a, st, c1[zd]);
+    const bool z = a.gate_up.z || a.down.z;
+    if (a.x_bf16) return z ? moe_launch<VW, true, 1>(a, st) : moe_launch<VW, false, 1>(a, st);
+    return z ? moe_launch<VW, true, kTerms>(a, st) : moe_launch<VW, false, kTerms>(a, st);
 }
 
 cudaError_t moe(const MoeArgs &args, cudaStream_t st) {
     MoeArgs a = args;
     a.svec_gate_up = scales_vec(a.gate_up, a.group);
     a.svec_down = scales_vec(a.down, a.group);
+    const dim3 grid((unsigned)a.E, (unsigned)ceil_div(a.B, kRouterTokens));
     if (a.x_bf16)
-        moe_router_kernel<__nv_bfloat16><<<(unsigned)a.B, 32 * kMoeWarps, 0, st>>>(a);
+        moe_logits_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
     else
-        moe_router_kernel<float><<<(unsigned)a.B, 32 * kMoeWarps, 0, st>>>(a);
+        moe_logits_kernel<float><<<grid, 256, 0, st>>>(a);
     count_launch();
-    auto run = a.group == 32 ? moe_experts<1> : a.group == 64 ? moe_experts<2> : moe_experts<4>;
-    return run(a, st);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (a.group == 32) return moe_experts<1>(a, st);
+    if (a.group == 64) return moe_experts<2>(a, st);
+    return moe_experts<4>(a, st);
 }
 
 }  // namespace w4

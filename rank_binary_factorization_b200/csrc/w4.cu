@@ -381,6 +381,7 @@ struct GemvProb {
     __device__ __forceinline__ int last_row(int, int) const { return m - 1; }
     __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
     __device__ __forceinline__ void begin(int) {}
+    __device__ __forceinline__ int tiles(int) const { return (cols + 7) / 8; }
     __device__ __forceinline__ const char *col(int j) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
         if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));

@@ -138,8 +138,8 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // The 8 warps are WR row groups of WK; the warps of a group split the k axis into contiguous
 // ranges of units and join in shared memory at the end of the job (WK = 8 where the axis has
 // units enough: the fewest rows a job, the most even spread of jobs over the SMs).  Every
-// warp runs its own ring of kStages asynchronous copies (one unit of its rows: 128 bytes of
-// codes a row) that carries on across jobs, so 16 MT kStages KB a CTA are on their way from
+// warp runs its own ring of kRowStages / MT asynchronous copies (one unit of its rows: 128
+// bytes of codes a row) that carries on across jobs, so 64 KB a CTA are on their way from
 // memory at any time and no warp waits for another within a job.  Scales and zero points of
 // a unit go to registers while the unit before it is worked on; the cursor that runs ahead
 // fetches a job's scales towards the SM when it enters the job.
@@ -158,16 +158,19 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 //
 // Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
 // begin(job) (before the first activation of the job is read), col(j) -> the lane's column of
-// n-tile j of that job (XS: byte offset of its first word in shared memory, else address), and
-// end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
+// n-tile j of that job (XS: byte offset of its first word in shared memory, else address),
+// tiles(job) -> n-tiles that have a column, ready() (called once, with the first copies under
+// way) and end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
 constexpr int kWarps = 8;
-constexpr int kStages = 3;
+constexpr int kRowStages = 4;                    // stages times row tiles of a ring
 template <int MT>
-NQ_HD constexpr int ring_bytes() { return kWarps * kStages * MT * 2048; }
-// K-axis ranges of a row group for n columns.
+NQ_HD constexpr int ring_bytes() { return kWarps * kRowStages * 2048; }
+// K-axis ranges of a row group for n columns: two units a warp where the axis has them, so that
+// a job's fixed cost (joining the warps, its first loads) is shared by some work.  By n alone: a
+// result does not depend on what else is in the call.
 NQ_HD int k_ranges(int64_t n) {
     const int64_t u = ceil_div(n, kUnit);
-    return u >= 8 ? 8 : u >= 4 ? 4 : u >= 2 ? 2 : 1;
+    return u >= 16 ? 8 : u >= 8 ? 4 : u >= 4 ? 2 : 1;
 }
 
 // Word c (0..3) of lane t in a half: group c / VW, word c % VW of its VW.
@@ -194,16 +197,17 @@ struct Scales {
             const void *ps = M.s + at, *pz = M.z + at;
             if constexpr (G == 2) {
                 s[0] = __ldg(static_cast<const uint32_t *>(ps));
-                if constexpr (Z) z[0] = __ldg(static_cast<const unsigned short *>(pz));
+                if constexpr (Z) z[0] = M.z ? __ldg(static_cast<const unsigned short *>(pz)) : 0x0808u;
             } else if constexpr (G == 4) {
                 const uint2 v = __ldg(static_cast<const uint2 *>(ps));
                 s[0] = v.x, s[1] = v.y;
-                if constexpr (Z) z[0] = __ldg(static_cast<const uint32_t *>(pz));
+                if constexpr (Z) z[0] = M.z ? __ldg(static_cast<const uint32_t *>(pz)) : 0x08080808u;
             } else {
                 const uint4 v = __ldg(static_cast<const uint4 *>(ps));
                 s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
                 if constexpr (Z) {
-                    const uint2 u = __ldg(static_cast<const uint2 *>(pz));
+                    const uint2 u = M.z ? __ldg(static_cast<const uint2 *>(pz))
+                                        : make_uint2(0x08080808u, 0x08080808u);
                     z[0] = u.x, z[1] = u.y;
                 }
             }
@@ -218,7 +222,7 @@ struct Scales {
             if (grp + i < M.ng) {
                 s[i / 2] |= (uint32_t)__ldg(reinterpret_cast<const unsigned short *>(M.s) + at + i)
                             << (16 * (i & 1));
-                if constexpr (Z) z[i / 4] |= (uint32_t)(__ldg(M.z + at + i)) << (8 * (i & 3));
+                if constexpr (Z) z[i / 4] |= (M.z ? (uint32_t)__ldg(M.z + at + i) : 8u) << (8 * (i & 3));
             }
     }
     __device__ __forceinline__ float scale(int i) const {
@@ -239,7 +243,7 @@ inline bool scales_vec(const Mat &M, int group) {
 template <int VW, bool Z, bool XS, int MT, int NT, class Prob>
 __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, int WK, char *ring) {
     constexpr int G = kUnit / (32 * VW);         // groups of a unit
-    constexpr int kStage = MT * 2048;
+    constexpr int kStage = MT * 2048, kStages = kRowStages / MT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int wr = warp / WK, wk = warp % WK;
@@ -308,10 +312,12 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
             }
     };
     const char *col[NT];                         // XS: shared-memory offsets
+    int nt = NT;
     uint4 x[NT][4];
     auto load_x = [&](int half) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; ++j) {
+            if (j > 0 && j >= nt) break;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 if constexpr (XS) {
@@ -327,11 +333,13 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
                         col[j] + (half * 16 + lane_word<VW>(t, c)) * 16);
                 }
             }
+        }
     };
     auto start = [&](int job) {
         P.begin(job);
 #pragma unroll
         for (int j = 0; j < NT; ++j) col[j] = P.col(j);
+        nt = P.tiles(job);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -406,6 +414,7 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
                                                 code_pair1(w0 >> 8, z0), code_pair1(w1 >> 8, z1)};
 #pragma unroll
                         for (int j = 0; j < NT; ++j) {
+                            if (j > 0 && j >= nt) break;
                             const uint4 b = x[j][gi * VW + v];
                             mma16816(c[m][j], a0, b.x, b.y);
                             mma16816(c[m][j], a1, b.z, b.w);
@@ -501,12 +510,16 @@ struct MoeArgs {
     Mat gate_up;               // E matrices of 2f x d, one after the other
     Mat down;                  // E matrices of d x f
     int group;
-    int svec_gate_up, svec_down;   // set by moe()
     float *Y;                  // [B][d]
-    int32_t *ids;              // [B][top_k]
-    float *weights;            // [B][top_k]
-    __nv_bfloat16 *xw;         // [B][1 or kTerms][padded(d)], word order
+    int32_t *ids;              // [B][top_k] or null
+    float *weights;            // [B][top_k] or null
+    // workspace
+    unsigned int *bar;         // two arrival counts
+    double *logits;            // [B][E]
+    uint4 *xw;                 // [B][1 or kTerms][padded(d) / 8], word order
     __nv_bfloat16 *h;          // [B top_k][kTerms][padded(f)], word order
+    float *part;               // [B top_k][d]: an expert's output for a pair, not weighted
+    int svec_gate_up, svec_down;   // set by moe()
 };
 cudaError_t moe(const MoeArgs &a, cudaStream_t st);
 
