@@ -1450,7 +1450,7 @@ struct MoeLayout {
             return o;
         };
         bar = take(2 * sizeof(unsigned int));
-        logits = take((size_t)B * E * 8);
+        logits = take((size_t)ceil_div(d, 1024) * B * E * 8);
         xw = take((size_t)B * (dt == NQ_BF16 ? 1 : w4::kTerms) * w4::padded(d) * 2);
         h = take((size_t)B * top_k * w4::kTerms * w4::padded(f) * 2);
         part = take((size_t)B * top_k * d * 4);

@@ -8,37 +8,45 @@ namespace nq {
 namespace w4 {
 
 constexpr int kMoeMaxPairs = NQ_MOE_MAX_TOKENS * NQ_MOE_MAX_TOP_K;
-constexpr int kRouterTokens = 8;       // tokens of a CTA of the router
+constexpr int kRouterTokens = 8;       // tokens and columns of a CTA of the router: a thread
+constexpr int kRouterThreads = 128;    // holds 8 columns of its expert and of each token
+constexpr int kRouterColumns = 8 * kRouterThreads;
 
 // ---- router logits, columns of X --------------------------------------------------------
-// CTA: one expert, up to 8 tokens; the sums are in FP64, so that which experts are chosen does
-// not depend on their order.  The CTAs together also write X's columns in word order and clear
-// the arrival counts of the kernel that follows.
+// CTA: one expert, up to 8 tokens, 1024 columns; the sums are in FP64 (the parts of a logit are
+// added up by ``choose``), so that which experts are chosen does not depend on their order.  The
+// CTAs together also write X's columns in word order and clear the arrival counts of the kernel
+// that follows.
 template <typename T>
-__global__ void __launch_bounds__(256) moe_logits_kernel(const MoeArgs a) {
-    __shared__ double red[8][kRouterTokens];
+__device__ __forceinline__ void load8(const T *p, int left, bool vec, T (&v)[8]) {
+    if (vec && left >= 8) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            reinterpret_cast<uint4 *>(v)[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : (T)0.f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRouterThreads) moe_logits_kernel(const MoeArgs a, int vec) {
+    __shared__ double red[kRouterThreads / 32][kRouterTokens];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int e = blockIdx.x, b0 = blockIdx.y * kRouterTokens;
     const int nb = min(kRouterTokens, a.B - b0);
+    const int k = blockIdx.z * kRouterColumns + threadIdx.x * 8, left = a.d - k;
     const T *X = static_cast<const T *>(a.X);
-    if (e == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.bar[threadIdx.x] = 0;
-    const T *r = static_cast<const T *>(a.router) + (int64_t)e * a.d;
-    double acc[kRouterTokens] = {};
-    for (int k = threadIdx.x; k < a.d; k += 256) {
-        const double rv = (double)(float)r[k];
+    __align__(16) T r[8], x[kRouterTokens][8];
+    load8(static_cast<const T *>(a.router) + (int64_t)e * a.d + k, left, vec, r);
 #pragma unroll
-        for (int b = 0; b < kRouterTokens; ++b)
-            if (b < nb) acc[b] += rv * (double)(float)X[(int64_t)(b0 + b) * a.d + k];
-    }
-#pragma unroll
-    for (int b = 0; b < kRouterTokens; ++b) {
-        if (b >= nb) break;
-        const double v = warp_sum(acc[b]);
-        if (lane == 0) red[warp][b] = v;
-    }
+    for (int b = 0; b < kRouterTokens; ++b)
+        if (b < nb) load8(X + (int64_t)(b0 + b) * a.d + k, left, vec, x[b]);
+    if (e == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) a.bar[threadIdx.x] = 0;
     const int words = (int)(padded(a.d) / 8);
-    const int ctas = gridDim.x * gridDim.y, cta = blockIdx.y * gridDim.x + blockIdx.x;
-    for (int o = cta * 256 + threadIdx.x; o < a.B * words; o += ctas * 256) {
+    const int ctas = gridDim.x * gridDim.y * gridDim.z,
+              cta = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+    for (int o = cta * kRouterThreads + threadIdx.x; o < a.B * words; o += ctas * kRouterThreads) {
         const int b = o / words, wd = o % words;
         if constexpr (sizeof(T) == 2) {
             a.xw[o] = x_word(X + (int64_t)b * a.d, wd * 8, a.d);
@@ -49,20 +57,39 @@ __global__ void __launch_bounds__(256) moe_logits_kernel(const MoeArgs a) {
             for (int t = 0; t < kTerms; ++t) a.xw[((int64_t)b * kTerms + t) * words + wd] = w[t];
         }
     }
+    double rd[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rd[i] = (double)(float)r[i];
+#pragma unroll
+    for (int b = 0; b < kRouterTokens; ++b) {
+        if (b >= nb) break;
+        double v = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += rd[i] * (double)(float)x[b][i];
+        v = warp_sum(v);
+        if (lane == 0) red[warp][b] = v;
+    }
     __syncthreads();
     if (threadIdx.x < nb) {
         double v = 0.0;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v += red[w][threadIdx.x];
-        a.logits[(int64_t)(b0 + threadIdx.x) * a.E + e] = v;
+        for (int w = 0; w < kRouterThreads / 32; ++w) v += red[w][threadIdx.x];
+        a.logits[((int64_t)blockIdx.z * a.B + b0 + threadIdx.x) * a.E + e] = v;
     }
 }
 
 // ---- choice of experts --------------------------------------------------------------------
 // One warp, one token: the top_k largest logits (ties: the lowest expert) and their weights.
-__device__ void choose(const MoeArgs &a, int b, short *ids, float *weights) {
+// logit: scratch of the warp, E values.
+__device__ void choose(const MoeArgs &a, int b, double *logit, short *ids, float *weights) {
     const int lane = threadIdx.x & 31;
-    const double *logit = a.logits + (int64_t)b * a.E;
+    const int slices = (a.d + kRouterColumns - 1) / kRouterColumns;
+    for (int e = lane; e < a.E; e += 32) {
+        double v = 0.0;
+        for (int s = 0; s < slices; ++s) v += a.logits[((int64_t)s * a.B + b) * a.E + e];
+        logit[e] = v;
+    }
+    __syncwarp();
     // lane l looks after experts l, l + 32, ...; the winner of each round leaves
     unsigned int gone = 0;
     double top = 0.0, sum = 0.0;
@@ -325,14 +352,18 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
                                                                          : sizeof(Red<1, ND>));
     Lists &L = *reinterpret_cast<Lists *>(sm + ring_bytes<1>() + kRed);
     const int pairs = a.B * a.top_k;
-    for (int b = threadIdx.x >> 5; b < a.B; b += kWarps) choose(a, b, L.ids, L.weights);
+    // (the ring of copies is not in use yet: scratch)
+    for (int b = threadIdx.x >> 5; b < a.B; b += kWarps) {
+        choose(a, b, reinterpret_cast<double *>(sm) + (threadIdx.x >> 5) * NQ_MOE_MAX_EXPERTS, L.ids,
+               L.weights);
+        __syncwarp();
+    }
     __syncthreads();
     if (blockIdx.x == 0)
         for (int p = threadIdx.x; p < pairs; p += 32 * kWarps) {
             if (a.ids) a.ids[p] = L.ids[p];
             if (a.weights) a.weights[p] = L.weights[p];
         }
-    // (the ring of copies is not in use yet)
     build_lists(L, reinterpret_cast<unsigned int(*)[2]>(sm), pairs, a.top_k, a.E);
     build_chunks(L, 8 * NU / TERMS);
     {
@@ -410,11 +441,14 @@ cudaError_t moe(const MoeArgs &args, cudaStream_t st) {
     MoeArgs a = args;
     a.svec_gate_up = scales_vec(a.gate_up, a.group);
     a.svec_down = scales_vec(a.down, a.group);
-    const dim3 grid((unsigned)a.E, (unsigned)ceil_div(a.B, kRouterTokens));
+    const dim3 grid((unsigned)a.E, (unsigned)ceil_div(a.B, kRouterTokens),
+                    (unsigned)ceil_div(a.d, kRouterColumns));
+    const int vec = (a.d * (a.x_bf16 ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
     if (a.x_bf16)
-        moe_logits_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a);
+        moe_logits_kernel<__nv_bfloat16><<<grid, kRouterThreads, 0, st>>>(a, vec);
     else
-        moe_logits_kernel<float><<<grid, 256, 0, st>>>(a);
+        moe_logits_kernel<float><<<grid, kRouterThreads, 0, st>>>(a, vec);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

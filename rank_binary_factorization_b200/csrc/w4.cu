@@ -491,7 +491,11 @@ static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, co
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit((const void *)kern, fixed + (XS ? kXsBytes : 0), configured);
     if (e != cudaSuccess) return e;
-    const int WK = k_ranges(M.n);
+    // fewer rows a job where the layer has too few of them to keep two CTAs an SM busy
+    int WK = k_ranges(M.n);
+    while (2 * WK <= kWarps && 2 * WK <= ceil_div(M.n, kUnit) &&
+           ceil_div(m, 16 * MT * (kWarps / WK)) < 2 * kNumSMsB200)
+        WK *= 2;
     const int64_t blocks = ceil_div(m, 16 * MT * (kWarps / WK)), chunks = ceil_div(B, 8 * NT / terms);
     int64_t ctas = 2 * (int64_t)device_sm_count() / chunks;
     ctas = ctas < 1 ? 1 : ctas > blocks ? blocks : ctas;

@@ -515,7 +515,7 @@ struct MoeArgs {
     float *weights;            // [B][top_k] or null
     // workspace
     unsigned int *bar;         // two arrival counts
-    double *logits;            // [B][E]
+    double *logits;            // [ceil(d / 1024)][B][E]: parts of a logit
     uint4 *xw;                 // [B][1 or kTerms][padded(d) / 8], word order
     __nv_bfloat16 *h;          // [B top_k][kTerms][padded(f)], word order
     float *part;               // [B top_k][d]: an expert's output for a pair, not weighted
