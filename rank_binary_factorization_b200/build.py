@@ -5,6 +5,8 @@
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -14,7 +16,7 @@ SOURCES = ["api.cu", "gemm_tc.cu", "kernels.cu", "chol.cu", "binary.cu", "calib_
 HEADERS = ["common.cuh", "gemm_tc.cuh", "kernels.cuh", "layout.h", "tc_ptx.cuh", "w4.cuh",
            os.path.join("..", "..", "include", "nq.h")]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
-              "-shared", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"]
+              "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"]
 
 
 def _nvcc():
@@ -36,13 +38,21 @@ def build(force=False, verbose=False):
     """Compile every CUDA source for sm_100a into libnq.so beside this file."""
     if not force and not stale():
         return LIB
-    cmd = [_nvcc()] + NVCC_FLAGS + ["-o", LIB + ".tmp"] + [os.path.join(CSRC, f) for f in SOURCES]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        sys.stderr.write(res.stdout + res.stderr)
-        raise RuntimeError("nvcc failed building libnq.so")
-    if verbose:
-        sys.stderr.write(res.stderr)
+    with tempfile.TemporaryDirectory() as tmp:
+        objects = [os.path.join(tmp, f + ".o") for f in SOURCES]
+        cmds = [[_nvcc()] + NVCC_FLAGS + ["-c", "-o", o, os.path.join(CSRC, f)]
+                for f, o in zip(SOURCES, objects)]
+        with ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+            runs = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), cmds))
+        if all(r.returncode == 0 for r in runs):
+            runs.append(subprocess.run([_nvcc()] + NVCC_FLAGS + ["-shared", "-o", LIB + ".tmp"] + objects,
+                                       capture_output=True, text=True))
+    for r in runs:
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr)
+            raise RuntimeError("nvcc failed building libnq.so")
+        if verbose:
+            sys.stderr.write(r.stderr)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

@@ -343,14 +343,14 @@ struct DownProb : ExpertJobs {
 // All CTAs of the launch are resident together (cooperative launch): choice and lists in every
 // CTA, gate and up jobs, arrival, down jobs, arrival, and y = sum over a token's choices of p times
 // the pair's output, in the order of the choices.
-template <int VW, bool Z, int TERMS>
+template <int VW, bool Z, bool SV, int TERMS>
 __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeArgs a) {
-    constexpr int NU = TERMS == 1 ? 1 : 2, ND = 2;
+    constexpr int NU = 1, ND = 2;
     extern __shared__ __align__(1024) char sm[];
-    void *red = sm + ring_bytes<1>();
+    void *red = sm + kRingBytes;
     constexpr size_t kRed = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
                                                                          : sizeof(Red<1, ND>));
-    Lists &L = *reinterpret_cast<Lists *>(sm + ring_bytes<1>() + kRed);
+    Lists &L = *reinterpret_cast<Lists *>(sm + kRingBytes + kRed);
     const int pairs = a.B * a.top_k;
     // (the ring of copies is not in use yet: scratch)
     for (int b = threadIdx.x >> 5; b < a.B; b += kWarps) {
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     build_chunks(L, 8 * NU / TERMS);
     {
         GateUpProb<NU> P(a, L, TERMS, 8 * NU / TERMS, static_cast<Red<2, NU> *>(red));
-        if (P.jobs > 0) run_products<VW, Z, false, 2, NU>(P, a.gate_up, a.svec_gate_up, P.WK, sm);
+        if (P.jobs > 0) run_products<VW, Z, SV, false, 2, NU>(P, a.gate_up, P.WK, sm);
     }
     __threadfence();
     arrive(a.bar);
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     {
         DownProb<ND> P(a, L, 8 * ND / kTerms, static_cast<Red<1, ND> *>(red));
         if (P.jobs > 0) {
-            run_products<VW, Z, false, 1, ND>(P, a.down, a.svec_down, P.WK, sm);
+            run_products<VW, Z, SV, false, 1, ND>(P, a.down, P.WK, sm);
             ok = P.ok;
         }
     }
@@ -395,13 +395,13 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     }
 }
 
-template <int VW, bool Z, int TERMS>
+template <int VW, bool Z, bool SV, int TERMS>
 static cudaError_t moe_launch(const MoeArgs &a, cudaStream_t st) {
-    constexpr int NU = TERMS == 1 ? 1 : 2, ND = 2;
+    constexpr int NU = 1, ND = 2;
     constexpr size_t red = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
                                                                         : sizeof(Red<1, ND>));
-    constexpr int smem = ring_bytes<1>() + (int)red + (int)sizeof(Lists);
-    auto kern = moe_experts_kernel<VW, Z, TERMS>;
+    constexpr int smem = kRingBytes + (int)red + (int)sizeof(Lists);
+    auto kern = moe_experts_kernel<VW, Z, SV, TERMS>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit((const void *)kern, smem, configured);
     if (e != cudaSuccess) return e;
@@ -430,17 +430,14 @@ static cudaError_t moe_launch(const MoeArgs &a, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <int VW>
+template <int VW, bool Z>
 static cudaError_t moe_experts(const MoeArgs &a, cudaStream_t st) {
-    const bool z = a.gate_up.z || a.down.z;
-    if (a.x_bf16) return z ? moe_launch<VW, true, 1>(a, st) : moe_launch<VW, false, 1>(a, st);
-    return z ? moe_launch<VW, true, kTerms>(a, st) : moe_launch<VW, false, kTerms>(a, st);
+    const bool sv = scales_vec(a.gate_up, a.group) && scales_vec(a.down, a.group);
+    if (a.x_bf16) return sv ? moe_launch<VW, Z, true, 1>(a, st) : moe_launch<VW, Z, false, 1>(a, st);
+    return sv ? moe_launch<VW, Z, true, kTerms>(a, st) : moe_launch<VW, Z, false, kTerms>(a, st);
 }
 
-cudaError_t moe(const MoeArgs &args, cudaStream_t st) {
-    MoeArgs a = args;
-    a.svec_gate_up = scales_vec(a.gate_up, a.group);
-    a.svec_down = scales_vec(a.down, a.group);
+cudaError_t moe(const MoeArgs &a, cudaStream_t st) {
     const dim3 grid((unsigned)a.E, (unsigned)ceil_div(a.B, kRouterTokens),
                     (unsigned)ceil_div(a.d, kRouterColumns));
     const int vec = (a.d * (a.x_bf16 ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 &&
@@ -452,9 +449,14 @@ cudaError_t moe(const MoeArgs &args, cudaStream_t st) {
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (a.group == 32) return moe_experts<1>(a, st);
-    if (a.group == 64) return moe_experts<2>(a, st);
-    return moe_experts<4>(a, st);
+    auto run = a.gate_up.z || a.down.z
+                   ? (a.group == 32   ? moe_experts<1, true>
+                      : a.group == 64 ? moe_experts<2, true>
+                                      : moe_experts<4, true>)
+                   : (a.group == 32   ? moe_experts<1, false>
+                      : a.group == 64 ? moe_experts<2, false>
+                                      : moe_experts<4, false>);
+    return run(a, st);
 }
 
 }  // namespace w4

@@ -404,10 +404,10 @@ struct GemvProb {
 // two CTAs an SM.
 constexpr int kXsBytes = 48 * 1024;
 
-template <int VW, bool Z, bool XS, int MT, int NT>
+template <int VW, bool Z, bool SV, bool XS, int MT, int NT>
 __global__ void __launch_bounds__(32 * kWarps, 2)
-    gemv_kernel(const Mat M, int m, const void *X, int x_bf16, const __nv_bfloat16 *xw, int svec,
-                int WK, int64_t B, int blocks, float *__restrict__ Y) {
+    gemv_kernel(const Mat M, int m, const void *X, int x_bf16, const __nv_bfloat16 *xw, int WK,
+                int64_t B, int blocks, float *__restrict__ Y) {
     extern __shared__ __align__(1024) char sm[];
     GemvProb<MT, NT, XS> P;
     P.jobs = (int)((blocks - blockIdx.x + gridDim.x - 1) / gridDim.x);
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     P.lrows = 31 - __clz(16 * MT * (kWarps / WK));
     P.ldx = padded(M.n);
     P.xw = XS ? nullptr : xw + P.b0 * P.terms * P.ldx;
-    P.red = reinterpret_cast<Red<MT, NT> *>(sm + ring_bytes<MT>());
+    P.red = reinterpret_cast<Red<MT, NT> *>(sm + kRingBytes);
     uint4 *xs = reinterpret_cast<uint4 *>(P.red + 2);
     P.xs = (uint32_t)__cvta_generic_to_shared(xs);
     P.half_stride = P.cols * 256;
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             }
         }
     }
-    run_products<VW, Z, XS, MT, NT>(P, M, svec, WK, sm);
+    run_products<VW, Z, SV, XS, MT, NT>(P, M, WK, sm);
 }
 
 // X (B x n) as columns in word order: [B][1 or kTerms][padded(n)].
@@ -481,13 +481,13 @@ size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B) {
     return x_bytes(n, x_bf16, B) + (B >= kTcRows ? tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes : 0);
 }
 
-template <int VW, bool Z, bool XS, int MT, int NT>
+template <int VW, bool Z, bool SV, bool XS, int MT, int NT>
 static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
                           int64_t B, float *Y, cudaStream_t st) {
     const int terms = x_bf16 ? 1 : kTerms;
-    constexpr int fixed = ring_bytes<MT>() + 2 * sizeof(Red<MT, NT>);
+    constexpr int fixed = kRingBytes + 2 * sizeof(Red<MT, NT>);
     const int smem = fixed + (XS ? (int)(B * terms * padded(M.n) * 2) : 0);
-    auto kern = gemv_kernel<VW, Z, XS, MT, NT>;
+    auto kern = gemv_kernel<VW, Z, SV, XS, MT, NT>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit((const void *)kern, fixed + (XS ? kXsBytes : 0), configured);
     if (e != cudaSuccess) return e;
@@ -500,18 +500,25 @@ static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, co
     int64_t ctas = 2 * (int64_t)device_sm_count() / chunks;
     ctas = ctas < 1 ? 1 : ctas > blocks ? blocks : ctas;
     kern<<<dim3((unsigned)ctas, (unsigned)chunks), 32 * kWarps, smem, st>>>(
-        M, (int)m, X, x_bf16, xw, scales_vec(M, 32 * VW), WK, B, (int)blocks, Y);
+        M, (int)m, X, x_bf16, xw, WK, B, (int)blocks, Y);
     count_launch();
     return cudaGetLastError();
+}
+
+template <int VW, bool Z, bool SV>
+static cudaError_t gemv_n(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
+                        int64_t B, float *Y, cudaStream_t st) {
+    if (x_shared(M.n, x_bf16, B)) return gemv_t<VW, Z, SV, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
+    if (B * (x_bf16 ? 1 : kTerms) <= 8)
+        return gemv_t<VW, Z, SV, false, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
+    return gemv_t<VW, Z, SV, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
 }
 
 template <int VW, bool Z>
 static cudaError_t gemv(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
                         int64_t B, float *Y, cudaStream_t st) {
-    if (x_shared(M.n, x_bf16, B)) return gemv_t<VW, Z, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
-    if (B * (x_bf16 ? 1 : kTerms) <= 8)
-        return gemv_t<VW, Z, false, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
-    return gemv_t<VW, Z, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
+    return scales_vec(M, 32 * VW) ? gemv_n<VW, Z, true>(M, m, X, x_bf16, xw, B, Y, st)
+                                  : gemv_n<VW, Z, false>(M, m, X, x_bf16, xw, B, Y, st);
 }
 
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,

@@ -75,6 +75,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {
                  "r"(in ? 16 : 0)
                  : "memory");
 }
+// 4 or 8 bytes (aligned), of which the first ``size`` are read.
+template <int N>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src, int size = N) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(size)
+                 : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_wait() {
@@ -140,9 +146,10 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // units enough: the fewest rows a job, the most even spread of jobs over the SMs).  Every
 // warp runs its own ring of kRowStages / MT asynchronous copies (one unit of its rows: 128
 // bytes of codes a row) that carries on across jobs, so 64 KB a CTA are on their way from
-// memory at any time and no warp waits for another within a job.  Scales and zero points of
-// a unit go to registers while the unit before it is worked on; the cursor that runs ahead
-// fetches a job's scales towards the SM when it enters the job.
+// memory at any time and no warp waits for another within a job.  Where the rows' scales and
+// zero points allow it (scales_vec) they come with the codes of their unit: loaded to registers
+// half a unit ahead, as they are for layers that do not, their latency took a quarter of the time
+// (11008x4096 g = 64 with zero points, one column: 15.0 us against 10.3 without the loads).
 //
 // The A fragment of an MMA is 16 rows of W (lane: rows lane/4 and lane/4 + 8), the B
 // fragment 8 columns (lane: column lane/4), so any order of the k axis serves as long as
@@ -154,7 +161,7 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // that the fragment loads (16, 8 or 4 bytes a lane for g = 128, 64, 32) meet every bank once.
 //
 // Columns past the last one repeat it: an MMA column reaches no other, and nobody reads its
-// sums.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
+// sums.  SV: scales_vec holds.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
 //
 // Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
 // begin(job) (before the first activation of the job is read), col(j) -> the lane's column of
@@ -163,8 +170,10 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // way) and end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
 constexpr int kWarps = 8;
 constexpr int kRowStages = 4;                    // stages times row tiles of a ring
-template <int MT>
-NQ_HD constexpr int ring_bytes() { return kWarps * kRowStages * 2048; }
+constexpr int kTileScales = 2048;                // in a stage of a tile: codes, then 16 bytes of
+constexpr int kTileZeros = 2048 + 256;           // scales and 8 of zero points a row
+constexpr int kTileBytes = 2048 + 256 + 128;
+constexpr int kRingBytes = kWarps * kRowStages * kTileBytes;
 // K-axis ranges of a row group for n columns: two units a warp where the axis has them, so that
 // a job's fixed cost (joining the warps, its first loads) is shared by some work.  By n alone: a
 // result does not depend on what else is in the call.
@@ -186,33 +195,13 @@ __device__ __forceinline__ int x_entry(int half, int wi, int col, int C) {
     return (half * C + col) * 16 + ((c ^ (col & 1)) << 2) + t;
 }
 
-// G scales (and zero points) of a row's unit, as registers; grp: the unit's first group.
+// G scales (and zero points) of a row's unit, as registers.
 template <int G, bool Z>
 struct Scales {
     static constexpr int NS = (G + 1) / 2, NZ = (G + 3) / 4;
     uint32_t s[NS], z[NZ];
-    // vec: every row's unit starts on a multiple of G scales and ends inside the row
-    __device__ __forceinline__ void load(const Mat &M, int64_t at, int grp, bool vec) {
-        if (vec) {
-            const void *ps = M.s + at, *pz = M.z + at;
-            if constexpr (G == 2) {
-                s[0] = __ldg(static_cast<const uint32_t *>(ps));
-                if constexpr (Z) z[0] = M.z ? __ldg(static_cast<const unsigned short *>(pz)) : 0x0808u;
-            } else if constexpr (G == 4) {
-                const uint2 v = __ldg(static_cast<const uint2 *>(ps));
-                s[0] = v.x, s[1] = v.y;
-                if constexpr (Z) z[0] = M.z ? __ldg(static_cast<const uint32_t *>(pz)) : 0x08080808u;
-            } else {
-                const uint4 v = __ldg(static_cast<const uint4 *>(ps));
-                s[0] = v.x, s[1] = v.y, s[2] = v.z, s[3] = v.w;
-                if constexpr (Z) {
-                    const uint2 u = M.z ? __ldg(static_cast<const uint2 *>(pz))
-                                        : make_uint2(0x08080808u, 0x08080808u);
-                    z[0] = u.x, z[1] = u.y;
-                }
-            }
-            return;
-        }
+    // one by one from global memory; grp: the unit's first group, at: its place
+    __device__ __forceinline__ void load(const Mat &M, int64_t at, int grp) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) s[i] = 0;
 #pragma unroll
@@ -225,6 +214,29 @@ struct Scales {
                 if constexpr (Z) z[i / 4] |= (M.z ? (uint32_t)__ldg(M.z + at + i) : 8u) << (8 * (i & 3));
             }
     }
+    // from a stage of the ring: row r of a tile
+    __device__ __forceinline__ void load(uint32_t tile, int r, bool zeros) {
+        const uint32_t ps = tile + kTileScales + r * 16, pz = tile + kTileZeros + r * 8;
+        if constexpr (G == 2) {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s[0]) : "r"(ps));
+        } else if constexpr (G == 4) {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "r"(ps));
+        } else {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3])
+                         : "r"(ps));
+        }
+        if constexpr (Z) {
+            if (!zeros) {
+#pragma unroll
+                for (int i = 0; i < NZ; ++i) z[i] = 0x08080808u;
+            } else if constexpr (G == 8) {
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(z[0]), "=r"(z[1]) : "r"(pz));
+            } else {
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(z[0]) : "r"(pz));
+            }
+        }
+    }
     __device__ __forceinline__ float scale(int i) const {
         return __uint_as_float(i & 1 ? s[i / 2] & 0xffff0000u : s[i / 2] << 16);
     }
@@ -233,17 +245,18 @@ struct Scales {
         return zero_point(8);
     }
 };
-// Whether Scales::load may take its vectors.
+// Whether the scales and zero points of a unit can be copied with its codes: every row's units
+// are whole and start on a multiple of their size (zero points at least 4 bytes).
 inline bool scales_vec(const Mat &M, int group) {
-    const int G = kUnit / group;
+    const int G = kUnit / group, GZ = G < 4 ? 4 : G;
     return M.ng % G == 0 && reinterpret_cast<uintptr_t>(M.s) % (2 * G) == 0 &&
-           reinterpret_cast<uintptr_t>(M.z) % G == 0;
+           reinterpret_cast<uintptr_t>(M.z) % GZ == 0;
 }
 
-template <int VW, bool Z, bool XS, int MT, int NT, class Prob>
-__device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, int WK, char *ring) {
+template <int VW, bool Z, bool SV, bool XS, int MT, int NT, class Prob>
+__device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char *ring) {
     constexpr int G = kUnit / (32 * VW);         // groups of a unit
-    constexpr int kStage = MT * 2048, kStages = kRowStages / MT;
+    constexpr int kStage = MT * kTileBytes, kStages = kRowStages / MT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int wr = warp / WK, wk = warp % WK;
@@ -264,6 +277,7 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
     }
     int pj = 0, pu = u0;
     const uint32_t *src[MT][4];
+    int64_t gat[MT];                             // lanes 0..15: the unit's first scale of that row
     auto enter = [&](int job) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
@@ -271,26 +285,38 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 src[m][i] = M.q + u0 * 32 + 4 * pc + (int64_t)min(first + pr + 4 * i, last) * M.ld;
-            // the job's scales: rows g and g + 8, 32 bytes a lane
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int grp = u0 * G + 16 * t;
-                if (grp < min(u1 * G, M.ng))
-                    asm volatile("prefetch.global.L1 [%0];" ::"l"(
-                        M.s + grp + (int64_t)min(first + g + 8 * h, last) * M.ng));
-            }
+            gat[m] = (int64_t)min(first + (lane & 15), last) * M.ng + u0 * G;
         }
     };
     auto issue = [&](uint32_t stage) {
         if (pj < P.jobs) {
             const bool in = pu * 32 + 4 * pc < M.ld;         // the row's words end here
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m) {
+                const uint32_t tile = stage + m * kTileBytes;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    copy16(stage + m * 2048 + put[i], src[m][i], in);
+                    copy16(tile + put[i], src[m][i], in);
                     src[m][i] += 32;
                 }
+                // lanes 0..15 the rows' scales, lanes 16..31 their zero points (G = 2: the
+                // aligned word that holds the two)
+                if constexpr (SV) {
+                    if (lane < 16) {
+                        if constexpr (G == 8)
+                            copy16(tile + kTileScales + lane * 16, M.s + gat[m], true);
+                        else
+                            copy_small<2 * G>(tile + kTileScales + lane * 16, M.s + gat[m]);
+                    } else if (Z && M.z) {
+                        if constexpr (G == 2)
+                            copy_small<4>(tile + kTileZeros + (lane & 15) * 8,
+                                          M.z + (gat[m] & ~int64_t(3)), 2 + (int)(gat[m] & 2));
+                        else
+                            copy_small<G>(tile + kTileZeros + (lane & 15) * 8, M.z + gat[m]);
+                    }
+                }
+                gat[m] += G;
+            }
             if (++pu == u1) {
                 pu = u0;
                 if (++pj < P.jobs) enter(pj);
@@ -299,17 +325,21 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
         copy_commit();
     };
 
-    // Consumer: scales of a unit, activations of a half, one step ahead of their use.
+    // Consumer: scales of a unit that do not come with the ring, activations of a half, one step
+    // ahead of their use.
     int64_t at[MT][2];                           // the unit's first scale of rows g and g + 8
     Scales<G, Z> sc[MT][2];
+    int zrow[MT][2];                             // place of a row's first zero point in its word
     auto load_scales = [&](int unit) {
+        if constexpr (!SV) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sc[m][h].load(M, at[m][h], unit * G, svec);
-                at[m][h] += G;
-            }
+                for (int h = 0; h < 2; ++h) {
+                    sc[m][h].load(M, at[m][h], unit * G);
+                    at[m][h] += G;
+                }
+        }
     };
     const char *col[NT];                         // XS: shared-memory offsets
     int nt = NT;
@@ -343,9 +373,12 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                at[m][h] = (int64_t)min(P.first_row(job, wr, m) + g + 8 * h, P.last_row(job, m)) * M.ng +
-                           u0 * G;
+            for (int h = 0; h < 2; ++h) {
+                const int64_t first = (int64_t)min(P.first_row(job, wr, m) + g + 8 * h, P.last_row(job, m)) *
+                                      M.ng;
+                if constexpr (!SV) at[m][h] = first + u0 * G;
+                zrow[m][h] = (int)first & 2;
+            }
         load_scales(u0);
         if constexpr (!XS) load_x(2 * u0);
     };
@@ -362,7 +395,17 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
         __syncwarp();
         Scales<G, Z> now[MT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) now[m][0] = sc[m][0], now[m][1] = sc[m][1];
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (SV) {
+                    now[m][h].load(stage + m * kTileBytes, g + 8 * h, M.z != nullptr);
+                    // the two zero points of a unit in their aligned word
+                    if (Z && G == 2 && M.z) now[m][h].z[0] >>= 8 * ((zrow[m][h] + unit * G) & 2);
+                } else {
+                    now[m][h] = sc[m][h];
+                }
+            }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t w[MT][2][4];
@@ -370,7 +413,7 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, bool svec, i
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t row = stage + m * 2048 + (8 * h + g) * 128;
+                    const uint32_t row = stage + m * kTileBytes + (8 * h + g) * 128;
                     if constexpr (VW == 4) {
                         asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                      : "=r"(w[m][h][0]), "=r"(w[m][h][1]), "=r"(w[m][h][2]),
@@ -519,7 +562,6 @@ struct MoeArgs {
     uint4 *xw;                 // [B][1 or kTerms][padded(d) / 8], word order
     __nv_bfloat16 *h;          // [B top_k][kTerms][padded(f)], word order
     float *part;               // [B top_k][d]: an expert's output for a pair, not weighted
-    int svec_gate_up, svec_down;   // set by moe()
 };
 cudaError_t moe(const MoeArgs &a, cudaStream_t st);
 
