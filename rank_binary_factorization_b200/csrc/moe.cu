@@ -29,7 +29,7 @@ __device__ __forceinline__ void load8(const T *p, int left, bool vec, T (&v)[8])
     }
 }
 
-template <typename T>
+template <typename T, int VW>
 __global__ void __launch_bounds__(kRouterThreads) moe_logits_kernel(const MoeArgs a, int vec) {
     __shared__ double red[kRouterThreads / 32][kRouterTokens];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -49,12 +49,15 @@ __global__ void __launch_bounds__(kRouterThreads) moe_logits_kernel(const MoeArg
     for (int o = cta * kRouterThreads + threadIdx.x; o < a.B * words; o += ctas * kRouterThreads) {
         const int b = o / words, wd = o % words;
         if constexpr (sizeof(T) == 2) {
-            a.xw[o] = x_word(X + (int64_t)b * a.d, wd * 8, a.d);
+            a.xw[(int64_t)b * words + x_word_place<VW>(wd, b)] = x_word(X + (int64_t)b * a.d, wd * 8, a.d);
         } else {
             uint4 w[kTerms];
             x_words(X + (int64_t)b * a.d, wd * 8, a.d, w);
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t) a.xw[((int64_t)b * kTerms + t) * words + wd] = w[t];
+            for (int t = 0; t < kTerms; ++t) {
+                const int64_t c = (int64_t)b * kTerms + t;
+                a.xw[c * words + x_word_place<VW>(wd, c)] = w[t];
+            }
         }
     }
     double rd[8];
@@ -268,7 +271,7 @@ struct ExpertJobs {
 
 // Gate and up projections: 16 rows of each side by side (two row tiles of a warp).  h leaves in
 // kTerms BF16 columns, its padding past f as zeros.
-template <int NT>
+template <int VW, int NT>
 struct GateUpProb : ExpertJobs {
     Red<2, NT> *red;
     int64_t ldh;
@@ -282,10 +285,12 @@ struct GateUpProb : ExpertJobs {
         return (expert(nth(job)) * 2 + i + 1) * a.f - 1;
     }
     __device__ __forceinline__ void ready() const {}
-    __device__ __forceinline__ const char *col(int j) const {
+    __device__ __forceinline__ const char *col(int j, bool &odd) const {
         int pair, term;
         column(j, pair, term);
-        return reinterpret_cast<const char *>(a.xw + ((int64_t)(pair / a.top_k) * terms + term) * ld);
+        const int64_t c = (int64_t)(pair / a.top_k) * terms + term;
+        odd = c & 1;
+        return reinterpret_cast<const char *>(a.xw + c * ld);
     }
     __device__ __forceinline__ void end(int job, const float (&acc)[2][NT][4]) {
         Red<2, NT> &R = red[job & 1];
@@ -299,8 +304,10 @@ struct GateUpProb : ExpertJobs {
             __nv_bfloat16 ht[kTerms];
             split_terms(k < a.f ? g / (1.f + expf(-g)) * u : 0.f, ht);
 #pragma unroll
-            for (int t = 0; t < kTerms; ++t)
-                a.h[((int64_t)L.pairs[p0 + p] * kTerms + t) * ldh + in_word(k)] = ht[t];
+            for (int t = 0; t < kTerms; ++t) {
+                const int64_t c = (int64_t)L.pairs[p0 + p] * kTerms + t;
+                a.h[c * ldh + x_word_place<VW>(k >> 3, c) * 8 + in_word(k & 7)] = ht[t];
+            }
         }
     }
 };
@@ -321,11 +328,12 @@ struct DownProb : ExpertJobs {
     }
     // the first copies of the weights are under way; h is complete when all CTAs have arrived
     __device__ __forceinline__ void ready() { ok = all_arrived(a.bar); }
-    __device__ __forceinline__ const char *col(int j) const {
+    __device__ __forceinline__ const char *col(int j, bool &odd) const {
         int pair, term;
         column(j, pair, term);
-        return reinterpret_cast<const char *>(reinterpret_cast<const uint4 *>(a.h) +
-                                              ((int64_t)pair * kTerms + term) * ld);
+        const int64_t c = (int64_t)pair * kTerms + term;
+        odd = c & 1;
+        return reinterpret_cast<const char *>(reinterpret_cast<const uint4 *>(a.h) + c * ld);
     }
     __device__ __forceinline__ void end(int job, const float (&acc)[1][NT][4]) {
         Red<1, NT> &R = red[job & 1];
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     build_lists(L, reinterpret_cast<unsigned int(*)[2]>(sm), pairs, a.top_k, a.E);
     build_chunks(L, 8 * NU / TERMS);
     {
-        GateUpProb<NU> P(a, L, TERMS, 8 * NU / TERMS, static_cast<Red<2, NU> *>(red));
+        GateUpProb<VW, NU> P(a, L, TERMS, 8 * NU / TERMS, static_cast<Red<2, NU> *>(red));
         if (P.jobs > 0) run_products<VW, Z, SV, false, 2, NU>(P, a.gate_up, P.WK, sm);
     }
     __threadfence();
@@ -442,10 +450,14 @@ cudaError_t moe(const MoeArgs &a, cudaStream_t st) {
                     (unsigned)ceil_div(a.d, kRouterColumns));
     const int vec = (a.d * (a.x_bf16 ? 2 : 4)) % 16 == 0 && reinterpret_cast<uintptr_t>(a.X) % 16 == 0 &&
                     reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
-    if (a.x_bf16)
-        moe_logits_kernel<__nv_bfloat16><<<grid, kRouterThreads, 0, st>>>(a, vec);
-    else
-        moe_logits_kernel<float><<<grid, kRouterThreads, 0, st>>>(a, vec);
+    using bf16 = __nv_bfloat16;
+    auto logits = a.x_bf16 ? (a.group == 32   ? moe_logits_kernel<bf16, 1>
+                              : a.group == 64 ? moe_logits_kernel<bf16, 2>
+                                              : moe_logits_kernel<bf16, 4>)
+                           : (a.group == 32   ? moe_logits_kernel<float, 1>
+                              : a.group == 64 ? moe_logits_kernel<float, 2>
+                                              : moe_logits_kernel<float, 4>);
+    logits<<<grid, kRouterThreads, 0, st>>>(a, vec);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -382,8 +382,9 @@ struct GemvProb {
     __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
     __device__ __forceinline__ void begin(int) {}
     __device__ __forceinline__ int tiles(int) const { return (cols + 7) / 8; }
-    __device__ __forceinline__ const char *col(int j) const {
+    __device__ __forceinline__ const char *col(int j, bool &odd) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
+        odd = (XS ? c : b0 * terms + c) & 1;
         if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));
         return reinterpret_cast<const char *>(xw + c * ldx);
     }
@@ -431,21 +432,24 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             const int b = o / words, wd = o % words;
             const int64_t row = (P.b0 + b) * M.n;
             if (x_bf16) {
-                xs[x_entry<VW>(wd / 16, wd % 16, b, P.cols)] =
+                xs[(wd / 16 * P.cols + b) * 16 + x_place<VW>(wd % 16, b & 1)] =
                     x_word(static_cast<const __nv_bfloat16 *>(X) + row, wd * 8, M.n);
             } else {
                 uint4 w[kTerms];
                 x_words(static_cast<const float *>(X) + row, wd * 8, M.n, w);
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-                    xs[x_entry<VW>(wd / 16, wd % 16, b * kTerms + t, P.cols)] = w[t];
+                for (int t = 0; t < kTerms; ++t) {
+                    const int c = b * kTerms + t;
+                    xs[(wd / 16 * P.cols + c) * 16 + x_place<VW>(wd % 16, c & 1)] = w[t];
+                }
             }
         }
     }
     run_products<VW, Z, SV, XS, MT, NT>(P, M, WK, sm);
 }
 
-// X (B x n) as columns in word order: [B][1 or kTerms][padded(n)].
+// X (B x n) as columns: [B][1 or kTerms][padded(n)], the words of a half placed for VW.
+template <int VW>
 __global__ void __launch_bounds__(256)
     x_words_kernel(const void *X, int x_bf16, int64_t B, int n, uint4 *__restrict__ xw) {
     const int words = (int)(padded(n) / 8);
@@ -453,12 +457,16 @@ __global__ void __launch_bounds__(256)
     const int wd = blockIdx.y * blockDim.x + threadIdx.x;
     if (wd >= words) return;
     if (x_bf16) {
-        xw[b * words + wd] = x_word(static_cast<const __nv_bfloat16 *>(X) + b * n, wd * 8, n);
+        xw[b * words + x_word_place<VW>(wd, b)] =
+            x_word(static_cast<const __nv_bfloat16 *>(X) + b * n, wd * 8, n);
     } else {
         uint4 w[kTerms];
         x_words(static_cast<const float *>(X) + b * n, wd * 8, n, w);
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t) xw[(b * kTerms + t) * words + wd] = w[t];
+        for (int t = 0; t < kTerms; ++t) {
+            const int64_t c = b * kTerms + t;
+            xw[c * words + x_word_place<VW>(wd, c)] = w[t];
+        }
     }
 }
 
@@ -510,7 +518,7 @@ static cudaError_t gemv_n(const Mat &M, int64_t m, const void *X, int x_bf16, co
                         int64_t B, float *Y, cudaStream_t st) {
     if (x_shared(M.n, x_bf16, B)) return gemv_t<VW, Z, SV, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
     if (B * (x_bf16 ? 1 : kTerms) <= 8)
-        return gemv_t<VW, Z, SV, false, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
+        return gemv_t<VW, Z, SV, false, 2, 1>(M, m, X, x_bf16, xw, B, Y, st);
     return gemv_t<VW, Z, SV, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
 }
 
@@ -524,7 +532,11 @@ static cudaError_t gemv(const Mat &M, int64_t m, const void *X, int x_bf16, cons
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st) {
     if (!x_shared(M.n, x_bf16, B)) {
-        x_words_kernel<<<dim3((unsigned)B, (unsigned)ceil_div(padded(M.n) / 8, 256)), 256, 0, st>>>(
+        auto words = B >= kTcRows   ? x_words_kernel<0>
+                     : group == 32  ? x_words_kernel<1>
+                     : group == 64  ? x_words_kernel<2>
+                                    : x_words_kernel<4>;
+        words<<<dim3((unsigned)B, (unsigned)ceil_div(padded(M.n) / 8, 256)), 256, 0, st>>>(
             X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw));
         count_launch();
     }

@@ -89,7 +89,8 @@ __device__ __forceinline__ void copy_wait() {
 
 // ---- activations -----------------------------------------------------------------------
 // The product reads a column of activations as BF16 words of 8 values in the order of the
-// code pairs, (0,4) (1,5) (2,6) (3,7), zero from n up to a multiple of kUnit.
+// code pairs, (0,4) (1,5) (2,6) (3,7), zero from n up to a multiple of kUnit; the 16 words of a
+// half unit in the order of x_place.
 constexpr int kUnit = 256;                       // columns of W in a unit of work
 constexpr int kHalf = 128;                       // a unit's halves: 4 words a lane
 NQ_HD int64_t padded(int64_t n) { return round_up(n, kUnit); }
@@ -164,8 +165,9 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // sums.  SV: scales_vec holds.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
 //
 // Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
-// begin(job) (before the first activation of the job is read), col(j) -> the lane's column of
-// n-tile j of that job (XS: byte offset of its first word in shared memory, else address),
+// begin(job) (before the first activation of the job is read), col(j, odd) -> the lane's
+// column of n-tile j of that job (XS: byte offset of its first word in shared memory, else
+// address) and whether it is an odd one (x_place),
 // tiles(job) -> n-tiles that have a column, ready() (called once, with the first copies under
 // way) and end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
 constexpr int kWarps = 8;
@@ -182,17 +184,20 @@ NQ_HD int k_ranges(int64_t n) {
     return u >= 16 ? 8 : u >= 8 ? 4 : u >= 4 ? 2 : 1;
 }
 
-// Word c (0..3) of lane t in a half: group c / VW, word c % VW of its VW.
+// Place of word wi of a half of a column (one of its 16 words of 16 bytes): word c of lane t lies
+// at 4 c + t, so that the lanes of a column read 64 consecutive bytes, and two neighbouring
+// columns ("odd") read different halves of the banks.
 template <int VW>
-NQ_HD int lane_word(int t, int c) { return (c / VW) * 4 * VW + t * VW + c % VW; }
-
-// Shared-memory place (in 16-byte entries) of word wi of a half of column ``col`` of C: the
-// lanes of an MMA read 16 bytes each, 4 t side by side, two columns in two halves of the banks.
-template <int VW>
-__device__ __forceinline__ int x_entry(int half, int wi, int col, int C) {
+__device__ __forceinline__ int x_place(int wi, int odd) {
     const int c = VW == 4 ? wi & 3 : VW == 2 ? (wi >> 3) * 2 + (wi & 1) : wi >> 2;
     const int t = VW == 4 ? wi >> 2 : VW == 2 ? (wi >> 1) & 3 : wi & 3;
-    return (half * C + col) * 16 + ((c ^ (col & 1)) << 2) + t;
+    return ((c ^ odd) << 2) + t;
+}
+// The same for word ``wd`` of a whole column (natural order for VW = 0, the tensor-memory path).
+template <int VW>
+__device__ __forceinline__ int x_word_place(int wd, int64_t col) {
+    if constexpr (VW == 0) return wd;
+    else return (wd & ~15) + x_place<VW>(wd & 15, (int)(col & 1));
 }
 
 // G scales (and zero points) of a row's unit, as registers.
@@ -342,6 +347,7 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
         }
     };
     const char *col[NT];                         // XS: shared-memory offsets
+    int odd[NT];                                 // 64 for an odd column (x_place)
     int nt = NT;
     uint4 x[NT][4];
     auto load_x = [&](int half) {
@@ -350,17 +356,15 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
             if (j > 0 && j >= nt) break;
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+                const int off = t * 16 + (c & 2) * 64 + ((c & 1) ? 64 - odd[j] : odd[j]);
                 if constexpr (XS) {
-                    // x_entry: words c of an odd column lie at c ^ 1
                     const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(col[j]) +
-                                       half * P.half_stride + t * 16 + (c & 2) * 64 +
-                                       ((c & 1) ? 64 - ((g & 1) << 6) : (g & 1) << 6);
+                                       half * P.half_stride + off;
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(x[j][c].x), "=r"(x[j][c].y), "=r"(x[j][c].z), "=r"(x[j][c].w)
                                  : "r"(a));
                 } else {
-                    x[j][c] = *reinterpret_cast<const uint4 *>(
-                        col[j] + (half * 16 + lane_word<VW>(t, c)) * 16);
+                    x[j][c] = *reinterpret_cast<const uint4 *>(col[j] + half * 256 + off);
                 }
             }
         }
@@ -368,7 +372,11 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
     auto start = [&](int job) {
         P.begin(job);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) col[j] = P.col(j);
+        for (int j = 0; j < NT; ++j) {
+            bool is_odd;
+            col[j] = P.col(j, is_odd);
+            odd[j] = is_odd ? 64 : 0;
+        }
         nt = P.tiles(job);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
