@@ -93,40 +93,40 @@ __device__ void choose(const MoeArgs &a, int b, double *logit, short *ids, float
         logit[e] = v;
     }
     __syncwarp();
-    // lane l looks after experts l, l + 32, ...; the winner of each round leaves
+    // Logits as whole numbers of the same order (NaNs above all others, or below); lane l looks
+    // after experts l, l + 32, ...; the winner of each round leaves.
     unsigned int gone = 0;
-    double top = 0.0, sum = 0.0;
     double mine = 0.0;     // lane j: the j-th chosen logit
     int chosen = 0;
     for (int j = 0; j < a.top_k; ++j) {
-        double best = 0.0;
-        int at = -1;
+        unsigned long long best = 0;
+        int at = 0x7fffffff;
         for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
             if (gone >> i & 1) continue;
-            const double v = logit[e];
-            if (at < 0 || v > best) best = v, at = e;
+            const long long v = __double_as_longlong(logit[e] + 0.0);      // -0 counts as 0
+            const unsigned long long key = v < 0 ? ~v : v | 1ll << 63;
+            if (at == 0x7fffffff || key > best) best = key, at = e;
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-            const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-            if (oa >= 0 && (at < 0 || ob > best || (!(best > ob) && oa < at))) best = ob, at = oa;
-        }
-        at = __shfl_sync(0xffffffffu, at, 0);   // one choice, also among NaNs
-        best = logit[at];
+        bool in = at != 0x7fffffff;
+        const unsigned int hi = __reduce_max_sync(0xffffffffu, in ? (unsigned int)(best >> 32) : 0u);
+        in = in && (unsigned int)(best >> 32) == hi;
+        const unsigned int lo = __reduce_max_sync(0xffffffffu, in ? (unsigned int)best : 0u);
+        in = in && (unsigned int)best == lo;
+        at = (int)__reduce_min_sync(0xffffffffu, in ? (unsigned int)at : 0x7fffffffu);
         if ((at & 31) == lane) gone |= 1u << (at >> 5);
-        if (j == 0) top = best;
-        sum += exp(best - top);
-        if (lane == j) mine = best, chosen = at;
+        if (lane == j) mine = logit[at], chosen = at;
     }
+    const double top = __shfl_sync(0xffffffffu, mine, 0);
+    const double p = lane < a.top_k ? exp(mine - top) : 0.0;
+    double sum = p;
     if (!a.renormalise) {
         sum = 0.0;
         for (int e = lane; e < a.E; e += 32) sum += exp(logit[e] - top);
-        sum = warp_sum(sum);
     }
+    sum = warp_sum(sum);
     if (lane < a.top_k) {
         ids[b * a.top_k + lane] = (short)chosen;
-        weights[b * a.top_k + lane] = (float)(exp(mine - top) / sum);
+        weights[b * a.top_k + lane] = (float)(p / sum);
     }
 }
 
@@ -254,17 +254,23 @@ struct ExpertJobs {
     }
     __device__ __forceinline__ int nth(int job) const { return blockIdx.x + job * gridDim.x; }
     __device__ __forceinline__ int expert(int n) const { return L.expert[L.chunk_active[n / blocks]]; }
+    __device__ __forceinline__ int chunk_pairs(int c) const {
+        return min(per, L.first[L.chunk_active[c] + 1] - L.chunk_first[c]);
+    }
     __device__ __forceinline__ void begin(int job) {
         const int n = nth(job), c = n / blocks;
         r0 = (n - c * blocks) << lrows;
         p0 = L.chunk_first[c];
-        np = min(per, L.first[L.chunk_active[c] + 1] - p0);
+        np = chunk_pairs(c);
     }
-    __device__ __forceinline__ int tiles(int) const { return (np * terms + 7) / 8; }
-    // the lane's column of n-tile j as (pair, term)
-    __device__ __forceinline__ void column(int j, int &pair, int &term) const {
-        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), np * terms - 1);
-        pair = L.pairs[p0 + c / terms];
+    __device__ __forceinline__ int tiles(int job) const {
+        return (chunk_pairs(nth(job) / blocks) * terms + 7) / 8;
+    }
+    // the lane's column of n-tile j of a job as (pair, term)
+    __device__ __forceinline__ void column(int job, int j, int &pair, int &term) const {
+        const int k = nth(job) / blocks;
+        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), chunk_pairs(k) * terms - 1);
+        pair = L.pairs[L.chunk_first[k] + c / terms];
         term = c % terms;
     }
 };
@@ -285,9 +291,9 @@ struct GateUpProb : ExpertJobs {
         return (expert(nth(job)) * 2 + i + 1) * a.f - 1;
     }
     __device__ __forceinline__ void ready() const {}
-    __device__ __forceinline__ const char *col(int j, bool &odd) const {
+    __device__ __forceinline__ const char *col(int job, int j, bool &odd) const {
         int pair, term;
-        column(j, pair, term);
+        column(job, j, pair, term);
         const int64_t c = (int64_t)(pair / a.top_k) * terms + term;
         odd = c & 1;
         return reinterpret_cast<const char *>(a.xw + c * ld);
@@ -328,9 +334,9 @@ struct DownProb : ExpertJobs {
     }
     // the first copies of the weights are under way; h is complete when all CTAs have arrived
     __device__ __forceinline__ void ready() { ok = all_arrived(a.bar); }
-    __device__ __forceinline__ const char *col(int j, bool &odd) const {
+    __device__ __forceinline__ const char *col(int job, int j, bool &odd) const {
         int pair, term;
-        column(j, pair, term);
+        column(job, j, pair, term);
         const int64_t c = (int64_t)pair * kTerms + term;
         odd = c & 1;
         return reinterpret_cast<const char *>(reinterpret_cast<const uint4 *>(a.h) + c * ld);

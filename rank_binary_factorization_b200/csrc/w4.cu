@@ -382,7 +382,7 @@ struct GemvProb {
     __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
     __device__ __forceinline__ void begin(int) {}
     __device__ __forceinline__ int tiles(int) const { return (cols + 7) / 8; }
-    __device__ __forceinline__ const char *col(int j, bool &odd) const {
+    __device__ __forceinline__ const char *col(int, int j, bool &odd) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
         odd = (XS ? c : b0 * terms + c) & 1;
         if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));

@@ -165,8 +165,7 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // sums.  SV: scales_vec holds.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
 //
 // Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
-// begin(job) (before the first activation of the job is read), col(j, odd) -> the lane's
-// column of n-tile j of that job (XS: byte offset of its first word in shared memory, else
+// begin(job) (before the job's end), col(job, j, odd) -> the lane's column of n-tile j of a job (XS: byte offset of its first word in shared memory, else
 // address) and whether it is an odd one (x_place),
 // tiles(job) -> n-tiles that have a column, ready() (called once, with the first copies under
 // way) and end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
@@ -369,15 +368,17 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
             }
         }
     };
-    auto start = [&](int job) {
-        P.begin(job);
+    auto columns_of = [&](int job) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             bool is_odd;
-            col[j] = P.col(j, is_odd);
+            col[j] = P.col(job, j, is_odd);
             odd[j] = is_odd ? 64 : 0;
         }
         nt = P.tiles(job);
+    };
+    auto start = [&](int job) {
+        P.begin(job);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -388,7 +389,6 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
                 zrow[m][h] = (int)first & 2;
             }
         load_scales(u0);
-        if constexpr (!XS) load_x(2 * u0);
     };
 
     enter(0);
@@ -396,6 +396,8 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
 #pragma unroll
     for (int s = 0; s < kStages; ++s) issue(base + s * kStage);
     P.ready();
+    columns_of(0);
+    if constexpr (!XS) load_x(2 * u0);
     start(0);
     float acc[MT][NT][4] = {};
     for (int job = 0, unit = u0;;) {
@@ -484,8 +486,14 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
                     }
                 }
             }
-            if constexpr (!XS)
-                if (half == 0 || unit + 1 < u1) load_x(2 * unit + half + 1);
+            if constexpr (!XS) {
+                if (half == 0 || unit + 1 < u1) {
+                    load_x(2 * unit + half + 1);
+                } else if (job + 1 < P.jobs) {   // the next job's first, while this one is joined
+                    columns_of(job + 1);
+                    load_x(2 * u0);
+                }
+            }
         }
         if (++unit < u1) continue;
         P.end(job, acc);
