@@ -240,37 +240,42 @@ struct ExpertJobs {
     const MoeArgs &a;
     const Lists &L;
     int terms, per, lrows, blocks;         // columns of a pair, pairs of a chunk, log2 rows of a block
+    int chunk_step, block_step;            // from one job of a CTA to the next
     int64_t ld;                            // 16-byte words of a column
-    int p0 = 0, np = 0, r0 = 0;            // the running job
+    struct Cursor {
+        int chunk, block;
+    };
 
-    __device__ ExpertJobs(const MoeArgs &a_, const Lists &L_, int n, int rows, int mt_rows, int terms_,
-                          int per_)
+    __device__ ExpertJobs(const MoeArgs &a_, const Lists &L_, int n, int rows, int terms_, int per_)
         : WK(k_ranges(n)), a(a_), L(L_), terms(terms_), per(per_) {
-        lrows = 31 - __clz(mt_rows * (kWarps / WK));
+        lrows = 31 - __clz(16 * (kWarps / WK));
         blocks = (rows + (1 << lrows) - 1) >> lrows;
+        chunk_step = gridDim.x / blocks;
+        block_step = gridDim.x % blocks;
         ld = padded(n) / 8;
         const int all = L.chunks * blocks;
         jobs = ((int)blockIdx.x < all) ? (all - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
     }
-    __device__ __forceinline__ int nth(int job) const { return blockIdx.x + job * gridDim.x; }
-    __device__ __forceinline__ int expert(int n) const { return L.expert[L.chunk_active[n / blocks]]; }
-    __device__ __forceinline__ int chunk_pairs(int c) const {
-        return min(per, L.first[L.chunk_active[c] + 1] - L.chunk_first[c]);
+    __device__ __forceinline__ Cursor first() const {
+        return {(int)blockIdx.x / blocks, (int)blockIdx.x % blocks};
     }
-    __device__ __forceinline__ void begin(int job) {
-        const int n = nth(job), c = n / blocks;
-        r0 = (n - c * blocks) << lrows;
-        p0 = L.chunk_first[c];
-        np = chunk_pairs(c);
+    __device__ __forceinline__ void next(Cursor &c) const {
+        c.chunk += chunk_step;
+        c.block += block_step;
+        if (c.block >= blocks) c.block -= blocks, ++c.chunk;
     }
-    __device__ __forceinline__ int tiles(int job) const {
-        return (chunk_pairs(nth(job) / blocks) * terms + 7) / 8;
+    // (a cursor past the last job is not looked at)
+    __device__ __forceinline__ int expert(const Cursor &c) const {
+        return L.expert[L.chunk_active[c.chunk]];
     }
+    __device__ __forceinline__ int pairs(const Cursor &c) const {
+        return min(per, L.first[L.chunk_active[c.chunk] + 1] - L.chunk_first[c.chunk]);
+    }
+    __device__ __forceinline__ int tiles(const Cursor &c) const { return (pairs(c) * terms + 7) / 8; }
     // the lane's column of n-tile j of a job as (pair, term)
-    __device__ __forceinline__ void column(int job, int j, int &pair, int &term) const {
-        const int k = nth(job) / blocks;
-        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), chunk_pairs(k) * terms - 1);
-        pair = L.pairs[L.chunk_first[k] + c / terms];
+    __device__ __forceinline__ void column(const Cursor &cur, int j, int &pair, int &term) const {
+        const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), pairs(cur) * terms - 1);
+        pair = L.pairs[L.chunk_first[cur.chunk] + c / terms];
         term = c % terms;
     }
 };
@@ -282,31 +287,34 @@ struct GateUpProb : ExpertJobs {
     Red<2, NT> *red;
     int64_t ldh;
     __device__ GateUpProb(const MoeArgs &a, const Lists &L, int terms, int per, Red<2, NT> *red_)
-        : ExpertJobs(a, L, a.d, (int)padded(a.f), 16, terms, per), red(red_), ldh(padded(a.f)) {}
-    __device__ __forceinline__ int first_row(int job, int wr, int i) const {
-        const int n = nth(job);
-        return (expert(n) * 2 + i) * a.f + (n % blocks << lrows) + wr * 16;
+        : ExpertJobs(a, L, a.d, (int)padded(a.f), terms, per), red(red_), ldh(padded(a.f)) {}
+    __device__ __forceinline__ int first_row(const Cursor &c, int wr, int i) const {
+        return (expert(c) * 2 + i) * a.f + (c.block << lrows) + wr * 16;
     }
-    __device__ __forceinline__ int last_row(int job, int i) const {
-        return (expert(nth(job)) * 2 + i + 1) * a.f - 1;
+    __device__ __forceinline__ int last_row(const Cursor &c, int i) const {
+        return (expert(c) * 2 + i + 1) * a.f - 1;
     }
     __device__ __forceinline__ void ready() const {}
-    __device__ __forceinline__ const char *col(int job, int j, bool &odd) const {
+    __device__ __forceinline__ const char *col(const Cursor &cur, int j, bool &odd) const {
         int pair, term;
-        column(job, j, pair, term);
+        column(cur, j, pair, term);
         const int64_t c = (int64_t)(pair / a.top_k) * terms + term;
         odd = c & 1;
         return reinterpret_cast<const char *>(a.xw + c * ld);
     }
-    __device__ __forceinline__ void end(int job, const float (&acc)[2][NT][4]) {
-        Red<2, NT> &R = red[job & 1];
+    __device__ __forceinline__ void end(const Cursor &cur, int job, const float (&acc)[2][NT][4]) {
+        // two of them used in turn, or one where they are large (two barriers a job)
+        const int wr = (threadIdx.x >> 5) / WK;
+        Red<2, NT> &R = red[NT == 1 ? job & 1 : 0];
+        if (NT > 1) group_sync(wr, WK);
         R.put(acc);
-        __syncthreads();
-        for (int o = threadIdx.x; o < np << lrows; o += 32 * kWarps) {
-            const int r = o & ((1 << lrows) - 1), p = o >> lrows, k = r0 + r;
+        group_sync(wr, WK);
+        const int r0 = (cur.block << lrows) + 16 * wr, np = pairs(cur), p0 = L.chunk_first[cur.chunk];
+        for (int o = threadIdx.x - wr * 32 * WK; o < 16 * np; o += 32 * WK) {
+            const int r = o % 16, p = o / 16, k = r0 + r;
             if (k >= ldh) continue;
-            const float g = R.sum(r / 16, WK, r % 16, p * terms, terms),
-                        u = R.sum(r / 16, WK, 16 + r % 16, p * terms, terms);
+            const float g = R.sum(wr, WK, r, p * terms, terms),
+                        u = R.sum(wr, WK, 16 + r, p * terms, terms);
             __nv_bfloat16 ht[kTerms];
             split_terms(k < a.f ? g / (1.f + expf(-g)) * u : 0.f, ht);
 #pragma unroll
@@ -324,46 +332,56 @@ struct DownProb : ExpertJobs {
     Red<1, NT> *red;
     bool ok = true;                        // all of h was there
     __device__ DownProb(const MoeArgs &a, const Lists &L, int per, Red<1, NT> *red_)
-        : ExpertJobs(a, L, a.f, a.d, 16, kTerms, per), red(red_) {}
-    __device__ __forceinline__ int first_row(int job, int wr, int) const {
-        const int n = nth(job);
-        return expert(n) * a.d + (n % blocks << lrows) + wr * 16;
+        : ExpertJobs(a, L, a.f, a.d, kTerms, per), red(red_) {}
+    __device__ __forceinline__ int first_row(const Cursor &c, int wr, int) const {
+        return expert(c) * a.d + (c.block << lrows) + wr * 16;
     }
-    __device__ __forceinline__ int last_row(int job, int) const {
-        return (expert(nth(job)) + 1) * a.d - 1;
+    __device__ __forceinline__ int last_row(const Cursor &c, int) const {
+        return (expert(c) + 1) * a.d - 1;
     }
     // the first copies of the weights are under way; h is complete when all CTAs have arrived
     __device__ __forceinline__ void ready() { ok = all_arrived(a.bar); }
-    __device__ __forceinline__ const char *col(int job, int j, bool &odd) const {
+    __device__ __forceinline__ const char *col(const Cursor &cur, int j, bool &odd) const {
         int pair, term;
-        column(job, j, pair, term);
+        column(cur, j, pair, term);
         const int64_t c = (int64_t)pair * kTerms + term;
         odd = c & 1;
         return reinterpret_cast<const char *>(reinterpret_cast<const uint4 *>(a.h) + c * ld);
     }
-    __device__ __forceinline__ void end(int job, const float (&acc)[1][NT][4]) {
+    __device__ __forceinline__ void end(const Cursor &cur, int job, const float (&acc)[1][NT][4]) {
         Red<1, NT> &R = red[job & 1];
         R.put(acc);
-        __syncthreads();
-        for (int o = threadIdx.x; o < np << lrows; o += 32 * kWarps) {
-            const int r = o & ((1 << lrows) - 1), p = o >> lrows;
+        const int wr = (threadIdx.x >> 5) / WK;
+        group_sync(wr, WK);
+        const int r0 = (cur.block << lrows) + 16 * wr, np = pairs(cur), p0 = L.chunk_first[cur.chunk];
+        for (int o = threadIdx.x - wr * 32 * WK; o < 16 * np; o += 32 * WK) {
+            const int r = o % 16, p = o / 16;
             if (r0 + r < a.d)
-                a.part[(int64_t)L.pairs[p0 + p] * a.d + r0 + r] =
-                    R.sum(r / 16, WK, r % 16, p * kTerms, kTerms);
+                a.part[(int64_t)L.pairs[p0 + p] * a.d + r0 + r] = R.sum(wr, WK, r, p * kTerms, kTerms);
         }
     }
 };
+
+// n-tiles of a job: BF16 tokens of an expert in eights, FP32 ones (three columns each) in fives, as
+// are the pairs of the down projection; a tile without columns costs nothing.
+constexpr int kDownTiles = 2;
+NQ_HD constexpr int moe_up_tiles(int terms) { return terms == 1 ? 1 : 2; }
+NQ_HD constexpr int moe_red_bytes(int terms) {
+    return terms == 1 ? 2 * (int)sizeof(Red<2, 1>) : (int)sizeof(Red<2, 2>);
+}
+static_assert(2 * sizeof(Red<1, kDownTiles>) <= 2 * sizeof(Red<2, 1>) &&
+                  2 * sizeof(Red<1, kDownTiles>) <= sizeof(Red<2, 2>),
+              "the down projection's sums fit where the others were");
 
 // All CTAs of the launch are resident together (cooperative launch): choice and lists in every
 // CTA, gate and up jobs, arrival, down jobs, arrival, and y = sum over a token's choices of p times
 // the pair's output, in the order of the choices.
 template <int VW, bool Z, bool SV, int TERMS>
 __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeArgs a) {
-    constexpr int NU = 1, ND = 2;
+    constexpr int NU = moe_up_tiles(TERMS), ND = kDownTiles;
     extern __shared__ __align__(1024) char sm[];
     void *red = sm + kRingBytes;
-    constexpr size_t kRed = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
-                                                                         : sizeof(Red<1, ND>));
+    constexpr int kRed = moe_red_bytes(TERMS);
     Lists &L = *reinterpret_cast<Lists *>(sm + kRingBytes + kRed);
     const int pairs = a.B * a.top_k;
     // (the ring of copies is not in use yet: scratch)
@@ -411,10 +429,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
 
 template <int VW, bool Z, bool SV, int TERMS>
 static cudaError_t moe_launch(const MoeArgs &a, cudaStream_t st) {
-    constexpr int NU = 1, ND = 2;
-    constexpr size_t red = 2 * (sizeof(Red<2, NU>) > sizeof(Red<1, ND>) ? sizeof(Red<2, NU>)
-                                                                        : sizeof(Red<1, ND>));
-    constexpr int smem = kRingBytes + (int)red + (int)sizeof(Lists);
+    constexpr int smem = kRingBytes + moe_red_bytes(TERMS) + (int)sizeof(Lists);
     auto kern = moe_experts_kernel<VW, Z, SV, TERMS>;
     static std::atomic<uint64_t> configured{0};
     cudaError_t e = ensure_smem_limit((const void *)kern, smem, configured);

@@ -372,31 +372,32 @@ struct GemvProb {
     Red<MT, NT> *red;                      // two, used in turn: one barrier per job
 
     // job k of a CTA is row block blockIdx.x + k gridDim.x of 16 MT (8 / WK) rows
-    __device__ __forceinline__ int block_row(int job) const {
-        return (int)(blockIdx.x + (unsigned)job * gridDim.x) << lrows;
+    struct Cursor {
+        int row;
+    };
+    __device__ __forceinline__ Cursor first() const { return {(int)blockIdx.x << lrows}; }
+    __device__ __forceinline__ void next(Cursor &c) const { c.row += gridDim.x << lrows; }
+    __device__ __forceinline__ int first_row(const Cursor &c, int wr, int i) const {
+        return c.row + 16 * (MT * wr + i);
     }
-    __device__ __forceinline__ int first_row(int job, int wr, int i) const {
-        return block_row(job) + 16 * (MT * wr + i);
-    }
-    __device__ __forceinline__ int last_row(int, int) const { return m - 1; }
+    __device__ __forceinline__ int last_row(const Cursor &, int) const { return m - 1; }
     __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
-    __device__ __forceinline__ void begin(int) {}
-    __device__ __forceinline__ int tiles(int) const { return (cols + 7) / 8; }
-    __device__ __forceinline__ const char *col(int, int j, bool &odd) const {
+    __device__ __forceinline__ int tiles(const Cursor &) const { return (cols + 7) / 8; }
+    __device__ __forceinline__ const char *col(const Cursor &, int j, bool &odd) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
         odd = (XS ? c : b0 * terms + c) & 1;
         if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));
         return reinterpret_cast<const char *>(xw + c * ldx);
     }
-    __device__ __forceinline__ void end(int job, const float (&acc)[MT][NT][4]) {
+    __device__ __forceinline__ void end(const Cursor &c, int job, const float (&acc)[MT][NT][4]) {
         Red<MT, NT> &R = red[job & 1];
         R.put(acc);
-        __syncthreads();
-        const int r0 = block_row(job);
-        for (int o = threadIdx.x; o < nb << lrows; o += 32 * kWarps) {
-            const int r = o & ((1 << lrows) - 1), b = o >> lrows;
-            if (r0 + r < m)
-                Y[(b0 + b) * m + r0 + r] = R.sum(r / (16 * MT), WK, r % (16 * MT), b * terms, terms);
+        const int wr = (threadIdx.x >> 5) / WK;
+        group_sync(wr, WK);
+        const int r0 = first_row(c, wr, 0);
+        for (int o = threadIdx.x - wr * 32 * WK; o < 16 * MT * nb; o += 32 * WK) {
+            const int r = o % (16 * MT), b = o / (16 * MT);
+            if (r0 + r < m) Y[(b0 + b) * m + r0 + r] = R.sum(wr, WK, r, b * terms, terms);
         }
     }
 };

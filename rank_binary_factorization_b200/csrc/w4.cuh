@@ -143,7 +143,7 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 //
 // A job is MT tiles of 16 rows, WR times over, against NT x 8 columns and the whole k axis.
 // The 8 warps are WR row groups of WK; the warps of a group split the k axis into contiguous
-// ranges of units and join in shared memory at the end of the job (WK = 8 where the axis has
+// ranges of units and join in shared memory at the end of the job, apart from the other groups (WK = 8 where the axis has
 // units enough: the fewest rows a job, the most even spread of jobs over the SMs).  Every
 // warp runs its own ring of kRowStages / MT asynchronous copies (one unit of its rows: 128
 // bytes of codes a row) that carries on across jobs, so 64 KB a CTA are on their way from
@@ -164,11 +164,12 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 // Columns past the last one repeat it: an MMA column reaches no other, and nobody reads its
 // sums.  SV: scales_vec holds.  XS: the CTA's columns lie in shared memory (stage_x), else in global memory.
 //
-// Prob supplies: jobs, first_row(job, group, tile) and last_row(job, tile) -> rows of M,
-// begin(job) (before the job's end), col(job, j, odd) -> the lane's column of n-tile j of a job (XS: byte offset of its first word in shared memory, else
-// address) and whether it is an odd one (x_place),
-// tiles(job) -> n-tiles that have a column, ready() (called once, with the first copies under
-// way) and end(job, acc) (every warp calls it once per job; acc is in units of 1 / kCodeUnit).
+// Prob supplies: jobs, a Cursor over them with first() and next(cursor), first_row(cursor, group,
+// tile) and last_row(cursor, tile) -> rows of M, col(cursor, j, odd) -> the lane's column of n-tile
+// j (XS: byte offset of its first word in shared memory, else address) and whether it is an odd
+// one (x_place), tiles(cursor) -> n-tiles that have a column, ready() (called once, with the first
+// copies under way) and end(cursor, job, acc) (every warp calls it once per job; acc is in units of
+// 1 / kCodeUnit).
 constexpr int kWarps = 8;
 constexpr int kRowStages = 4;                    // stages times row tiles of a ring
 constexpr int kTileScales = 2048;                // in a stage of a tile: codes, then 16 bytes of
@@ -280,12 +281,13 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
         put[i] = r * 128 + ((pc ^ sw) << 4);
     }
     int pj = 0, pu = u0;
+    typename Prob::Cursor pcur = P.first();
     const uint32_t *src[MT][4];
     int64_t gat[MT];                             // lanes 0..15: the unit's first scale of that row
-    auto enter = [&](int job) {
+    auto enter = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const int first = P.first_row(job, wr, m), last = P.last_row(job, m);
+            const int first = P.first_row(pcur, wr, m), last = P.last_row(pcur, m);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 src[m][i] = M.q + u0 * 32 + 4 * pc + (int64_t)min(first + pr + 4 * i, last) * M.ld;
@@ -323,7 +325,10 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
             }
             if (++pu == u1) {
                 pu = u0;
-                if (++pj < P.jobs) enter(pj);
+                if (++pj < P.jobs) {
+                    P.next(pcur);
+                    enter();
+                }
             }
         }
         copy_commit();
@@ -368,22 +373,22 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
             }
         }
     };
-    auto columns_of = [&](int job) {
+    auto columns_of = [&](const typename Prob::Cursor &cur) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             bool is_odd;
-            col[j] = P.col(job, j, is_odd);
+            col[j] = P.col(cur, j, is_odd);
             odd[j] = is_odd ? 64 : 0;
         }
-        nt = P.tiles(job);
+        nt = P.tiles(cur);
     };
-    auto start = [&](int job) {
-        P.begin(job);
+    typename Prob::Cursor cur = pcur, after = pcur;      // the running job, the one after it
+    auto start = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int64_t first = (int64_t)min(P.first_row(job, wr, m) + g + 8 * h, P.last_row(job, m)) *
+                const int64_t first = (int64_t)min(P.first_row(cur, wr, m) + g + 8 * h, P.last_row(cur, m)) *
                                       M.ng;
                 if constexpr (!SV) at[m][h] = first + u0 * G;
                 zrow[m][h] = (int)first & 2;
@@ -391,14 +396,15 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
         load_scales(u0);
     };
 
-    enter(0);
+    enter();
     uint32_t stage = base;
 #pragma unroll
     for (int s = 0; s < kStages; ++s) issue(base + s * kStage);
     P.ready();
-    columns_of(0);
+    columns_of(cur);
     if constexpr (!XS) load_x(2 * u0);
-    start(0);
+    start();
+    P.next(after);
     float acc[MT][NT][4] = {};
     for (int job = 0, unit = u0;;) {
         copy_wait<kStages - 1>();
@@ -490,16 +496,18 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
                 if (half == 0 || unit + 1 < u1) {
                     load_x(2 * unit + half + 1);
                 } else if (job + 1 < P.jobs) {   // the next job's first, while this one is joined
-                    columns_of(job + 1);
+                    columns_of(after);
                     load_x(2 * u0);
                 }
             }
         }
         if (++unit < u1) continue;
-        P.end(job, acc);
+        P.end(cur, job, acc);
         unit = u0;
         if (++job == P.jobs) return;
-        start(job);
+        cur = after;
+        P.next(after);
+        start();
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -507,6 +515,11 @@ __device__ __forceinline__ void run_products(Prob &P, const Mat &M, int WK, char
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
     }
+}
+
+// The WK warps of row group wr wait for one another.
+__device__ __forceinline__ void group_sync(int wr, int WK) {
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + wr), "r"(32 * WK) : "memory");
 }
 
 // The warps' sums of a job side by side in shared memory: v[warp][row][column].
