@@ -6,6 +6,7 @@ calls the library of the same name; all computation runs in the CUDA kernels of
 ``libnq.so``.  Importing this package without the built library raises ImportError.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -181,12 +182,12 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 def _w4_call(fn, dev, *args):
     """Call a library function on the current stream of device ``dev``."""
     if dev == torch.cuda.current_device():
-        code = getattr(lib, fn)(*args, _raw_stream(dev))
+        code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = getattr(lib, fn)(*args, _raw_stream(dev))
-    if code != _lib.NQ_OK:
-        raise NQError(fn, code)
+            code = fn(*args, _raw_stream(dev))
+    if code:
+        raise NQError(fn.__name__, code)
 
 
 def _w4_group(group):
@@ -197,17 +198,18 @@ def _w4_group(group):
 def _w4_layer(what, packed, scales, zeros, rows, n, group, dev):
     """Check one packed array: ``rows`` (its leading dimensions) rows of ``n`` columns."""
     _w4_group(group)
-    words, groups = rows + ((n + 31) // 32 * 4,), rows + ((n + group - 1) // group,)
+    words, groups = (*rows, (n + 31) // 32 * 4), (*rows, (n + group - 1) // group)
     if packed.dtype != torch.int32 or scales.dtype != torch.bfloat16 or \
             zeros is not None and zeros.dtype != torch.uint8:
         raise TypeError(f"{what}: codes must be int32, scales bfloat16 and zeros uint8")
     if packed.shape != words or scales.shape != groups or zeros is not None and zeros.shape != groups:
         raise ValueError(f"{what}: {n} columns in groups of {group} need codes of shape {words}, "
                          f"scales and zeros of shape {groups}")
-    for t in (packed, scales, zeros):
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            raise ValueError(f"{what}: codes, scales and zeros must be contiguous and on the "
-                             "device of the input")
+    if packed.get_device() != dev or scales.get_device() != dev or not packed.is_contiguous() or \
+            not scales.is_contiguous() or \
+            zeros is not None and (zeros.get_device() != dev or not zeros.is_contiguous()):
+        raise ValueError(f"{what}: codes, scales and zeros must be contiguous and on the device of "
+                         "the input")
 
 
 def _w4_input(x, name, dims):
@@ -221,6 +223,11 @@ def _w4_input(x, name, dims):
     if dt is None:
         raise TypeError(f"unsupported dtype {x.dtype}: use float32 or bfloat16")
     return x.get_device(), dt
+
+
+@functools.lru_cache(maxsize=4096)
+def _w4_workspace_size(m, n, dt, B):
+    return lib.nq_w4_workspace_size(m, n, dt, B)
 
 
 def _w4_ws(ws, need, dev):
@@ -250,7 +257,7 @@ def nq_w4_quantize(W, group=128, d_in=None, symmetric=True, grid=1):
     packed = W.new_empty((m, (n + 31) // 32 * 4), dtype=torch.int32)
     scales = W.new_empty((m, ng), dtype=torch.bfloat16)
     zeros = None if symmetric else W.new_empty((m, ng), dtype=torch.uint8)
-    _w4_call("nq_w4_quantize", dev, W.data_ptr(), dt, m, n,
+    _w4_call(lib.nq_w4_quantize, dev, W.data_ptr(), dt, m, n,
              None if d_in is None else d_in.data_ptr(), group, grid, packed.data_ptr(),
              scales.data_ptr(), None if zeros is None else zeros.data_ptr())
     return dict(packed=packed, scales=scales, zeros=zeros)
@@ -263,7 +270,7 @@ def nq_w4_dequantize(packed, scales, n, group=128, zeros=None, dtype=torch.float
     dev, m = packed.get_device(), packed.shape[0]
     _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
     W = packed.new_empty((m, n), dtype=dtype)
-    _w4_call("nq_w4_dequantize", dev, packed.data_ptr(), scales.data_ptr(),
+    _w4_call(lib.nq_w4_dequantize, dev, packed.data_ptr(), scales.data_ptr(),
              None if zeros is None else zeros.data_ptr(), m, n, group, W.data_ptr(), _dtype(W))
     return W
 
@@ -271,13 +278,13 @@ def nq_w4_dequantize(packed, scales, n, group=128, zeros=None, dtype=torch.float
 def nq_w4_matmul(packed, scales, X, group=128, zeros=None, ws=None):
     """Y = X W^T for a 4-bit layer and X of shape (B, n) or (n,); returns float32 Y."""
     dev, dt = _w4_input(X, "X", (1, 2))
-    n = X.shape[-1]
-    B = X.shape[0] if X.dim() == 2 else 1
+    shape = X.shape
+    n, B = shape[-1], 1 if len(shape) == 1 else shape[0]
     m = packed.shape[0]
     _w4_layer("packed", packed, scales, zeros, (m,), n, group, dev)
-    Y = X.new_empty((B, m) if X.dim() == 2 else (m,), dtype=torch.float32)
-    ws_ptr, ws_bytes = _w4_ws(ws, lib.nq_w4_workspace_size(m, n, dt, B), dev)
-    _w4_call("nq_w4_matmul", dev, packed.data_ptr(), scales.data_ptr(),
+    Y = X.new_empty((m,) if len(shape) == 1 else (B, m), dtype=torch.float32)
+    ws_ptr, ws_bytes = _w4_ws(ws, _w4_workspace_size(m, n, dt, B), dev)
+    _w4_call(lib.nq_w4_matmul, dev, packed.data_ptr(), scales.data_ptr(),
              None if zeros is None else zeros.data_ptr(), m, n, group, X.data_ptr(), dt, B,
              Y.data_ptr(), ws_ptr, ws_bytes)
     return Y
@@ -310,7 +317,7 @@ def nq_moe_w4(X, router, gate_up, gate_up_scales, down, down_scales, top_k, grou
     if need == 0:
         raise NQError("nq_moe_workspace_size", _lib.NQ_ERR_INVALID_ARG)
     ws_ptr, ws_bytes = _w4_ws(ws, need, dev)
-    _w4_call("nq_moe_w4", dev, X.data_ptr(), dt, B, d, router.data_ptr(), E, top_k,
+    _w4_call(lib.nq_moe_w4, dev, X.data_ptr(), dt, B, d, router.data_ptr(), E, top_k,
              1 if renormalise else 0, gate_up.data_ptr(), gate_up_scales.data_ptr(),
              None if gate_up_zeros is None else gate_up_zeros.data_ptr(), down.data_ptr(),
              down_scales.data_ptr(), None if down_zeros is None else down_zeros.data_ptr(), f,

@@ -359,7 +359,7 @@ cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf
 // ---------------------------------------------------------------------------------
 // Matrix product for few columns: persistent CTAs walk the row tiles (run_products).
 // ---------------------------------------------------------------------------------
-template <int MT, int NT, bool XS>
+template <int VW, int MT, int NT, bool XS>
 struct GemvProb {
     int jobs, WK;
     int terms, nb, cols;                   // columns per row of X; rows of X, columns of this CTA
@@ -368,6 +368,9 @@ struct GemvProb {
     const __nv_bfloat16 *xw;               // its columns (global memory), ldx apart
     int64_t ldx;
     uint32_t xs, half_stride;              // its columns (shared memory)
+    uint4 *xs_words;
+    const void *X;                         // what they are made from
+    int x_bf16, n;
     float *Y;
     Red<MT, NT> *red;                      // two, used in turn: one barrier per job
 
@@ -381,7 +384,50 @@ struct GemvProb {
         return c.row + 16 * (MT * wr + i);
     }
     __device__ __forceinline__ int last_row(const Cursor &, int) const { return m - 1; }
-    __device__ __forceinline__ void ready() const { if constexpr (XS) __syncthreads(); }
+    // XS: the CTA's columns into shared memory, while the first codes are on their way
+    __device__ __forceinline__ void ready() const {
+        if constexpr (XS) {
+            // words of all columns one after another, a few of a thread under way at a time
+            const int words = (int)(ldx / 8);
+            constexpr int AHEAD = 4;
+            int b = threadIdx.x / words, wd = threadIdx.x % words;
+            while (b < nb) {
+                int bs[AHEAD], ws[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    bs[i] = b, ws[i] = wd;
+                    wd += 32 * kWarps;
+                    while (wd >= words) wd -= words, ++b;
+                }
+                if (x_bf16) {
+                    uint4 v[AHEAD];
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i)
+                        if (bs[i] < nb)
+                            v[i] = x_word(static_cast<const __nv_bfloat16 *>(X) + (b0 + bs[i]) * n,
+                                          ws[i] * 8, n);
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i)
+                        if (bs[i] < nb)
+                            xs_words[(ws[i] / 16 * cols + bs[i]) * 16 + x_place<VW>(ws[i] % 16, bs[i] & 1)] =
+                                v[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < AHEAD; ++i) {
+                        if (bs[i] >= nb) break;
+                        uint4 w[kTerms];
+                        x_words(static_cast<const float *>(X) + (b0 + bs[i]) * n, ws[i] * 8, n, w);
+#pragma unroll
+                        for (int t = 0; t < kTerms; ++t) {
+                            const int c = bs[i] * kTerms + t;
+                            xs_words[(ws[i] / 16 * cols + c) * 16 + x_place<VW>(ws[i] % 16, c & 1)] = w[t];
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
     __device__ __forceinline__ int tiles(const Cursor &) const { return (cols + 7) / 8; }
     __device__ __forceinline__ const char *col(const Cursor &, int j, bool &odd) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
@@ -402,16 +448,17 @@ struct GemvProb {
     }
 };
 
-// Whether the columns of a CTA are kept in shared memory: up to this many bytes of them leave
-// two CTAs an SM.
-constexpr int kXsBytes = 48 * 1024;
+// Columns of a CTA that are kept in shared memory, bytes at most: what leaves two CTAs an SM
+// (4096x4096, 4 columns of 8 KB: 8.0 us from global memory with two, 11.4 us with one).
+constexpr int kXsBytes = 18 * 1024;
+static_assert(2 * (kRingBytes + 2 * (int)sizeof(Red<1, 2>) + kXsBytes + 1024) <= 228 * 1024, "two CTAs");
 
 template <int VW, bool Z, bool SV, bool XS, int MT, int NT>
 __global__ void __launch_bounds__(32 * kWarps, 2)
     gemv_kernel(const Mat M, int m, const void *X, int x_bf16, const __nv_bfloat16 *xw, int WK,
                 int64_t B, int blocks, float *__restrict__ Y) {
     extern __shared__ __align__(1024) char sm[];
-    GemvProb<MT, NT, XS> P;
+    GemvProb<VW, MT, NT, XS> P;
     P.jobs = (int)((blocks - blockIdx.x + gridDim.x - 1) / gridDim.x);
     P.WK = WK;
     P.terms = x_bf16 ? 1 : kTerms;
@@ -424,28 +471,10 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     P.ldx = padded(M.n);
     P.xw = XS ? nullptr : xw + P.b0 * P.terms * P.ldx;
     P.red = reinterpret_cast<Red<MT, NT> *>(sm + kRingBytes);
-    uint4 *xs = reinterpret_cast<uint4 *>(P.red + 2);
-    P.xs = (uint32_t)__cvta_generic_to_shared(xs);
+    P.X = X, P.x_bf16 = x_bf16, P.n = M.n;
+    P.xs_words = reinterpret_cast<uint4 *>(P.red + 2);
+    P.xs = (uint32_t)__cvta_generic_to_shared(P.xs_words);
     P.half_stride = P.cols * 256;
-    if constexpr (XS) {
-        const int words = (int)(P.ldx / 8);
-        for (int o = threadIdx.x; o < words * P.nb; o += 32 * kWarps) {
-            const int b = o / words, wd = o % words;
-            const int64_t row = (P.b0 + b) * M.n;
-            if (x_bf16) {
-                xs[(wd / 16 * P.cols + b) * 16 + x_place<VW>(wd % 16, b & 1)] =
-                    x_word(static_cast<const __nv_bfloat16 *>(X) + row, wd * 8, M.n);
-            } else {
-                uint4 w[kTerms];
-                x_words(static_cast<const float *>(X) + row, wd * 8, M.n, w);
-#pragma unroll
-                for (int t = 0; t < kTerms; ++t) {
-                    const int c = b * kTerms + t;
-                    xs[(wd / 16 * P.cols + c) * 16 + x_place<VW>(wd % 16, c & 1)] = w[t];
-                }
-            }
-        }
-    }
     run_products<VW, Z, SV, XS, MT, NT>(P, M, WK, sm);
 }
 
@@ -474,7 +503,7 @@ __global__ void __launch_bounds__(256)
 // Columns of X in the call, and whether a CTA keeps its own in shared memory.
 static bool x_shared(int64_t n, int x_bf16, int64_t B) {
     const int64_t cols = B * (x_bf16 ? 1 : kTerms);
-    return cols <= 8 && cols * padded(n) * 2 <= kXsBytes;
+    return cols <= 16 && cols * padded(n) * 2 <= kXsBytes;
 }
 
 // Rows of X from which the tensor-memory path (w4_tc.cu) takes the call.
@@ -517,10 +546,12 @@ static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, co
 template <int VW, bool Z, bool SV>
 static cudaError_t gemv_n(const Mat &M, int64_t m, const void *X, int x_bf16, const __nv_bfloat16 *xw,
                         int64_t B, float *Y, cudaStream_t st) {
-    if (x_shared(M.n, x_bf16, B)) return gemv_t<VW, Z, SV, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st);
-    if (B * (x_bf16 ? 1 : kTerms) <= 8)
-        return gemv_t<VW, Z, SV, false, 2, 1>(M, m, X, x_bf16, xw, B, Y, st);
-    return gemv_t<VW, Z, SV, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
+    const int64_t cols = B * (x_bf16 ? 1 : kTerms);
+    if (x_shared(M.n, x_bf16, B))
+        return cols <= 8 ? gemv_t<VW, Z, SV, true, 1, 1>(M, m, X, x_bf16, xw, B, Y, st)
+                         : gemv_t<VW, Z, SV, true, 1, 2>(M, m, X, x_bf16, xw, B, Y, st);
+    return cols <= 8 ? gemv_t<VW, Z, SV, false, 2, 1>(M, m, X, x_bf16, xw, B, Y, st)
+                     : gemv_t<VW, Z, SV, false, 2, 2>(M, m, X, x_bf16, xw, B, Y, st);
 }
 
 template <int VW, bool Z>

@@ -124,8 +124,16 @@ __device__ __forceinline__ void split_terms(float x, __nv_bfloat16 (&t)[kTerms])
 // The same of an FP32 vector: the words of its kTerms columns.
 __device__ __forceinline__ void x_words(const float *x, int64_t k, int n, uint4 (&w)[kTerms]) {
     __nv_bfloat16 t[8][kTerms];
+    __align__(16) float v[8];
+    if (k + 8 <= n && (reinterpret_cast<uintptr_t>(x + k) & 15) == 0) {
+        *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(x + k);
+        *reinterpret_cast<float4 *>(v + 4) = *reinterpret_cast<const float4 *>(x + k + 4);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split_terms(k + i < n ? x[k + i] : 0.f, t[i]);
+        for (int i = 0; i < 8; ++i) v[i] = k + i < n ? x[k + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) split_terms(v[i], t[i]);
 #pragma unroll
     for (int j = 0; j < kTerms; ++j) {
         uint32_t h[8];

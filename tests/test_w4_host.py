@@ -57,7 +57,7 @@ def test_moe_refuses():
 
 
 def test_workspace_sizes():
-    assert L.nq_w4_workspace_size(64, 64, 0, 3) > 0
+    assert L.nq_w4_workspace_size(64, 64, 0, 99) > 0
     assert L.nq_w4_workspace_size(64, 64, 0, 0) == 0
     assert L.nq_w4_workspace_size(0, 64, 0, 1) == 0
     small, large = (L.nq_moe_workspace_size(b, 64, 32, 4, 2, 0) for b in (1, 64))
