@@ -282,30 +282,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int q = warp & 3;
         uint32_t it = 0;
         bool ok = true;
+        auto hand_over = [&](uint32_t s) {
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+        };
         for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
             int k0, k1;
             stages_of(unit, k0, k1);
             const int row = min(unit / a.parts / a.ntiles * BM + 32 * q + lane, a.m - 1);
             const uint32_t *src = a.M.q + (int64_t)row * a.M.ld;
             const uint8_t *zeros = a.M.z + (int64_t)row * a.M.ng;
-            auto load = [&](int k, uint4 (&w)[4]) {
+            auto load = [&](int k, uint4 (&w)[4], uint32_t (&z)[GROUPS]) {
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g)
+                    z[g] = a.M.z ? __ldg(zeros + min(k * GROUPS + g, a.M.ng - 1)) : 8u;
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     w[c] = k < k1 && k * 16 + 4 * c < a.M.ld
                                ? __ldg(reinterpret_cast<const uint4 *>(src + k * 16 + 4 * c))
                                : make_uint4(0, 0, 0, 0);
             };
-            uint4 w[2][4];
-            load(k0, w[0]);
-            load(k0 + 1, w[1]);
+            uint4 w[2][4];                       // this stage and the next
+            uint32_t zv[2][GROUPS];
+            load(k0, w[0], zv[0]);
+            load(k0 + 1, w[1], zv[1]);
             for (int k = k0; k < k1 && ok; k += 2) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (k + i >= k1) break;
-                    uint32_t zv[GROUPS];
-#pragma unroll
-                    for (int g = 0; g < GROUPS; ++g)
-                        zv[g] = a.M.z ? __ldg(zeros + min((k + i) * GROUPS + g, a.M.ng - 1)) : 8u;
                     uint32_t r[2][32];
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -313,13 +319,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int c = 0; c < 8; ++c) {
                             const uint4 v = w[i][2 * h + c / 4];
                             const uint32_t x = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
-                            const ZeroPoint z = zero_point(zv[(8 * h + c) * 8 / GROUP] & 15u);
+                            const ZeroPoint z = zero_point(zv[i][(8 * h + c) * 8 / GROUP] & 15u);
                             r[h][4 * c] = code_pair0(x, z);
                             r[h][4 * c + 1] = code_pair1(x, z);
                             r[h][4 * c + 2] = code_pair0(x >> 8, z);
                             r[h][4 * c + 3] = code_pair1(x >> 8, z);
                         }
-                    load(k + i + 2, w[i]);
+                    load(k + i + 2, w[i], zv[i]);
+                    // a stage is handed over once the next one is decoded: its stores to TMEM
+                    // have had that time
+                    if (it > 0) hand_over((it - 1) % kRing);
                     const uint32_t s = it % kRing;
                     if (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane)) {
                         ok = false;
@@ -329,14 +338,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), r[h]);
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[s]);
                     ++it;
                 }
             }
         }
+        if (ok && it > 0) hand_over((it - 1) % kRing);
     }
     tc_fence_before();
     __syncthreads();
