@@ -1047,6 +1047,21 @@ bool make_map_bf16(CUtensorMap *map, const void *base, int64_t rows, int64_t col
     return r == CUDA_SUCCESS;
 }
 
+bool make_map_u32(CUtensorMap *map, const void *base, int64_t rows, int64_t words, int box_words,
+                  int box_rows) {
+    auto encode = get_encode();
+    if (!encode) return false;
+    if ((reinterpret_cast<uintptr_t>(base) & 15) || (words * 4) % 16) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)words, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)(words * 4)};
+    cuuint32_t box[2] = {(cuuint32_t)box_words, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides,
+                        box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 template <int BN, int STAGES, int EPI, bool F3>
 static cudaError_t launch_t(const Maps &maps, const EpiParams &p, cudaStream_t s) {
     constexpr int smem = STAGES * (F3 ? 2 : 1) * (A_TILE_BYTES + BN * BK * 2) + 1024 + 256;

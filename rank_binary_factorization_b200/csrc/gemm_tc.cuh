@@ -128,6 +128,11 @@ struct EpiParams {
 bool make_map_bf16(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
                    int box_rows);
 
+// Host: the same over rows of ``words`` 32-bit words, a box of box_words (64 bytes) x box_rows
+// with 64-byte swizzle.
+bool make_map_u32(CUtensorMap *map, const void *base, int64_t rows, int64_t words, int box_words,
+                  int box_rows);
+
 // Host: launch one GEMM.  BN in {64, 128, 256}.
 cudaError_t launch_gemm(const Maps &maps, const EpiParams &p, int epi, int BN, cudaStream_t s);
 

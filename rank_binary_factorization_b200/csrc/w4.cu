@@ -362,12 +362,11 @@ cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf
 template <int VW, int MT, int NT, bool XS>
 struct GemvProb {
     int jobs, WK;
-    int terms, nb, cols;                   // columns per row of X; rows of X, columns of this CTA
+    int terms, nb, cols;                   // columns per row of X; rows of X, their columns
     int m, lrows;                          // rows of W; log2 of the rows of a job
-    int64_t b0;                            // its first row of X
-    const __nv_bfloat16 *xw;               // its columns (global memory), ldx apart
+    const __nv_bfloat16 *xw;               // the columns (global memory), ldx apart
     int64_t ldx;
-    uint32_t xs, half_stride;              // its columns (shared memory)
+    uint32_t xs, half_stride;              // the columns (shared memory)
     uint4 *xs_words;
     const void *X;                         // what they are made from
     int x_bf16, n;
@@ -404,7 +403,7 @@ struct GemvProb {
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i)
                         if (bs[i] < nb)
-                            v[i] = x_word(static_cast<const __nv_bfloat16 *>(X) + (b0 + bs[i]) * n,
+                            v[i] = x_word(static_cast<const __nv_bfloat16 *>(X) + (int64_t)bs[i] * n,
                                           ws[i] * 8, n);
 #pragma unroll
                     for (int i = 0; i < AHEAD; ++i)
@@ -416,7 +415,7 @@ struct GemvProb {
                     for (int i = 0; i < AHEAD; ++i) {
                         if (bs[i] >= nb) break;
                         uint4 w[kTerms];
-                        x_words(static_cast<const float *>(X) + (b0 + bs[i]) * n, ws[i] * 8, n, w);
+                        x_words(static_cast<const float *>(X) + (int64_t)bs[i] * n, ws[i] * 8, n, w);
 #pragma unroll
                         for (int t = 0; t < kTerms; ++t) {
                             const int c = bs[i] * kTerms + t;
@@ -431,7 +430,7 @@ struct GemvProb {
     __device__ __forceinline__ int tiles(const Cursor &) const { return (cols + 7) / 8; }
     __device__ __forceinline__ const char *col(const Cursor &, int j, bool &odd) const {
         const int c = min(8 * j + (((int)threadIdx.x & 31) >> 2), cols - 1);
-        odd = (XS ? c : b0 * terms + c) & 1;
+        odd = c & 1;
         if constexpr (XS) return reinterpret_cast<const char *>((uintptr_t)(xs + c * 256));
         return reinterpret_cast<const char *>(xw + c * ldx);
     }
@@ -443,7 +442,7 @@ struct GemvProb {
         const int r0 = first_row(c, wr, 0);
         for (int o = threadIdx.x - wr * 32 * WK; o < 16 * MT * nb; o += 32 * WK) {
             const int r = o % (16 * MT), b = o / (16 * MT);
-            if (r0 + r < m) Y[(b0 + b) * m + r0 + r] = R.sum(wr, WK, r, b * terms, terms);
+            if (r0 + r < m) Y[(int64_t)b * m + r0 + r] = R.sum(wr, WK, r, b * terms, terms);
         }
     }
 };
@@ -462,14 +461,12 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     P.jobs = (int)((blocks - blockIdx.x + gridDim.x - 1) / gridDim.x);
     P.WK = WK;
     P.terms = x_bf16 ? 1 : kTerms;
-    const int per = 8 * NT / P.terms;
-    P.b0 = (int64_t)blockIdx.y * per;
-    P.nb = (int)min((int64_t)per, B - P.b0);
+    P.nb = B;
     P.cols = P.nb * P.terms;
     P.m = m, P.Y = Y;
     P.lrows = 31 - __clz(16 * MT * (kWarps / WK));
     P.ldx = padded(M.n);
-    P.xw = XS ? nullptr : xw + P.b0 * P.terms * P.ldx;
+    P.xw = xw;
     P.red = reinterpret_cast<Red<MT, NT> *>(sm + kRingBytes);
     P.X = X, P.x_bf16 = x_bf16, P.n = M.n;
     P.xs_words = reinterpret_cast<uint4 *>(P.red + 2);
@@ -500,14 +497,19 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Columns of the call above which the tensor-memory path (w4_tc.cu) takes it: the most that this
+// one holds at a time.  28672x8192: 16 BF16 rows 51 us here, 17 there 65; 8 FP32 rows (24 columns,
+// the codes twice) 85 us here, 67 there.  4096x4096, 8 FP32 rows: 12.1 here, 13.3 there.
+constexpr int kMaxColumns = 16;
+static bool on_tensor_memory(int x_bf16, int64_t B) {
+    return B * (x_bf16 ? 1 : kTerms) > kMaxColumns;
+}
+
 // Columns of X in the call, and whether a CTA keeps its own in shared memory.
 static bool x_shared(int64_t n, int x_bf16, int64_t B) {
     const int64_t cols = B * (x_bf16 ? 1 : kTerms);
-    return cols <= 16 && cols * padded(n) * 2 <= kXsBytes;
+    return cols <= kMaxColumns && cols * padded(n) * 2 <= kXsBytes;
 }
-
-// Rows of X from which the tensor-memory path (w4_tc.cu) takes the call.
-constexpr int64_t kTcRows = 17;
 
 static size_t x_bytes(int64_t n, int x_bf16, int64_t B) {
     const size_t b = (size_t)B * (x_bf16 ? 1 : kTerms) * padded(n) * 2;
@@ -516,7 +518,7 @@ static size_t x_bytes(int64_t n, int x_bf16, int64_t B) {
 
 size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B) {
     if (x_shared(n, x_bf16, B)) return 0;
-    return x_bytes(n, x_bf16, B) + (B >= kTcRows ? tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes : 0);
+    return x_bytes(n, x_bf16, B) + (on_tensor_memory(x_bf16, B) ? tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes : 0);
 }
 
 template <int VW, bool Z, bool SV, bool XS, int MT, int NT>
@@ -534,11 +536,9 @@ static cudaError_t gemv_t(const Mat &M, int64_t m, const void *X, int x_bf16, co
     while (2 * WK <= kWarps && 2 * WK <= ceil_div(M.n, kUnit) &&
            ceil_div(m, 16 * MT * (kWarps / WK)) < 2 * kNumSMsB200)
         WK *= 2;
-    const int64_t blocks = ceil_div(m, 16 * MT * (kWarps / WK)), chunks = ceil_div(B, 8 * NT / terms);
-    int64_t ctas = 2 * (int64_t)device_sm_count() / chunks;
-    ctas = ctas < 1 ? 1 : ctas > blocks ? blocks : ctas;
-    kern<<<dim3((unsigned)ctas, (unsigned)chunks), 32 * kWarps, smem, st>>>(
-        M, (int)m, X, x_bf16, xw, WK, B, (int)blocks, Y);
+    const int64_t blocks = ceil_div(m, 16 * MT * (kWarps / WK)), slots = 2 * (int64_t)device_sm_count();
+    kern<<<(unsigned)(blocks < slots ? blocks : slots), 32 * kWarps, smem, st>>>(
+        M, (int)m, X, x_bf16, xw, WK, (int)B, (int)blocks, Y);
     count_launch();
     return cudaGetLastError();
 }
@@ -564,15 +564,15 @@ static cudaError_t gemv(const Mat &M, int64_t m, const void *X, int x_bf16, cons
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st) {
     if (!x_shared(M.n, x_bf16, B)) {
-        auto words = B >= kTcRows   ? x_words_kernel<0>
-                     : group == 32  ? x_words_kernel<1>
-                     : group == 64  ? x_words_kernel<2>
-                                    : x_words_kernel<4>;
+        auto words = on_tensor_memory(x_bf16, B) ? x_words_kernel<0>
+                     : group == 32 ? x_words_kernel<1>
+                     : group == 64 ? x_words_kernel<2>
+                                   : x_words_kernel<4>;
         words<<<dim3((unsigned)B, (unsigned)ceil_div(padded(M.n) / 8, 256)), 256, 0, st>>>(
             X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw));
         count_launch();
     }
-    if (B >= kTcRows)
+    if (on_tensor_memory(x_bf16, B))
         return tc_matmul(M, m, group, xw, x_bf16 ? 1 : kTerms, B, Y,
                          reinterpret_cast<float *>(reinterpret_cast<char *>(xw) + x_bytes(M.n, x_bf16, B)),
                          st);

@@ -8,12 +8,14 @@
 // never runs longer than a group.  At g = 128 and BN = 128 a drain costs 128 FMAs a thread
 // against 512 clocks of MMA.
 //
-// Persistent, one CTA an SM, fourteen warps around one ring of kRing stages of 128 columns of k:
+// Persistent, one CTA an SM, nineteen warps around one ring of kRing stages of 128 columns of k:
 //   warp 0      TMA: X (BN rows, kTerms times for FP32) into shared memory (128-byte swizzle)
 //   warp 1      MMA issuer (M = 128, N = BN, K = 16, A from TMEM, B from shared memory)
 //   warps 2-9   drain: thread = row of W, half of its BN sums in registers; stores
-//   warps 10-13 decode: thread = row of W; codes go from global memory through registers into
+//   warps 10-17 decode: thread = row of W; codes go from shared memory through registers into
 //               the A operand in TMEM (lane = row, two columns of k a word)
+//   warp 18     TMA: the codes, 64 bytes a row and stage, into a ring of their own (64-byte
+//               swizzle: a warp's 16-byte loads down its rows meet every bank once)
 // One barrier says that a stage is full (the bytes of X and the four decoding warps), one that
 // it is empty: every wait and every commit of the issuing thread costs it about 50 clocks, and
 // with separate rings for both operands and 64 columns a stage it was issue that bound the
@@ -33,10 +35,12 @@ namespace w4 {
 using namespace tc;
 
 constexpr int kDrainWarps = 8;                   // two to a quarter of the tile's rows, half the columns each
-constexpr int kTcThreads = 32 * (2 + kDrainWarps + 4);
+constexpr int kDecodeWarps = 8;                  // two to a quarter of the rows, stages in turn
+constexpr int kTcThreads = 32 * (2 + kDrainWarps + kDecodeWarps + 1);
 constexpr int kRing = 4;                         // stages
 constexpr int kStageK = 128;                     // columns of k of a stage
 constexpr int kStageA = kStageK / 2;             // TMEM columns of a stage of the A operand
+constexpr int kCodeBytes = BM * kStageK / 2;     // codes of a stage: 64 bytes a row
 constexpr int kSplitUnit = kUnit / kStageK;      // stages of the least part of a split k axis
 
 struct TcArgs {
@@ -49,6 +53,7 @@ struct TcArgs {
 };
 struct TcMaps {
     CUtensorMap x[kTerms];
+    CUtensorMap codes;         // [m][ld] words, 16 x 128 a box, 64-byte swizzle
 };
 
 // 32 words a lane into TMEM.
@@ -118,8 +123,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// Stages of the ring of codes: it runs ahead of the other one, so that codes come from memory
+// well before they are decoded.
+NQ_HD constexpr int tc_code_stages(int BN, int T) { return BN * T > 128 ? 4 : 8; }
 template <int BN, int T>
-constexpr int tc_smem() { return kRing * T * BN * kStageK * 2 + 1024 + 256; }
+constexpr int tc_smem() {
+    return kRing * T * BN * kStageK * 2 + tc_code_stages(BN, T) * kCodeBytes + 1024 + 256;
+}
 
 // GS: MMA steps (16 columns of k) of a group.
 template <int BN, int T, int GS>
@@ -128,19 +138,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr int HALF = BN * BK * 2;            // bytes of 64 columns of BN rows of X
     constexpr int STAGE = T * 2 * HALF;
     constexpr int GROUP = 16 * GS, GROUPS = kStageK / GROUP;
+    constexpr int CODES = tc_code_stages(BN, T);
     constexpr uint32_t TMEM_COLS = 512;          // two accumulators of BN columns, the A ring
     static_assert(2 * BN + kRing * kStageA <= 512, "tensor memory");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kRing * STAGE);
-    uint64_t *empty = full + kRing, *d_full = empty + kRing, *d_empty = d_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(d_empty + 2);
+    uint8_t *codes = smem + kRing * STAGE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(codes + CODES * kCodeBytes);
+    uint64_t *empty = full + kRing, *d_full = empty + kRing, *d_empty = d_full + 2,
+             *c_full = d_empty + 2, *c_empty = c_full + CODES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_empty + CODES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 5), mbar_init(&empty[s], 1);
         for (int s = 0; s < 2; ++s) mbar_init(&d_full[s], 1), mbar_init(&d_empty[s], kDrainWarps);
+        for (int s = 0; s < CODES; ++s) mbar_init(&c_full[s], 1), mbar_init(&c_empty[s], 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -228,7 +242,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (warp < 2 + kDrainWarps) {
         // drain: rows of quarter q, columns c0 .. c0 + COLS - 1
-        constexpr int COLS = BN / 2, LD = COLS < 32 ? COLS : 32;
+        constexpr int COLS = BN / 2, LD = COLS == 32 ? 32 : 16;
         const int q = warp & 3, c0 = (warp - 2) / 4 * COLS;
         uint32_t grp = 0;
         bool dead = false;
@@ -255,19 +269,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 tc_fence_after();
                 const uint32_t base = tmem + (grp & 1) * BN + c0 + ((uint32_t)(32 * q) << 16);
-                uint32_t v[COLS / LD][LD];
 #pragma unroll
-                for (int c = 0; c < COLS / LD; ++c) tmem_ld(base + c * LD, v[c]);
+                for (int c = 0; c < COLS; c += LD) {
+                    uint32_t v[LD];
+                    tmem_ld(base + c, v);
+                    tmem_ld_wait(v);
 #pragma unroll
-                for (int c = 0; c < COLS / LD; ++c) tmem_ld_wait(v[c]);
+                    for (int j = 0; j < LD; j += 2) fma2(acc[(c + j) / 2], s, v[j], v[j + 1]);
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&d_empty[grp & 1]);
-                // (the accumulator is free for the next group but one while its sums are taken)
-#pragma unroll
-                for (int c = 0; c < COLS / LD; ++c)
-#pragma unroll
-                    for (int j = 0; j < LD; j += 2) fma2(acc[(c * LD + j) / 2], s, v[c][j], v[c][j + 1]);
             }
             if (row < a.m) {
                 float *dst = a.out + ((int64_t)(unit % a.parts) * a.B + n0) * a.m + row;
@@ -277,72 +289,80 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (n0 + j < a.B) dst[(int64_t)j * a.m] = f * (j & 1 ? acc[j / 2].y : acc[j / 2].x);
             }
         }
-    } else {
-        // decode
-        const int q = warp & 3;
-        uint32_t it = 0;
-        bool ok = true;
-        auto hand_over = [&](uint32_t s) {
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-        };
-        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
-            int k0, k1;
-            stages_of(unit, k0, k1);
-            const int row = min(unit / a.parts / a.ntiles * BM + 32 * q + lane, a.m - 1);
-            const uint32_t *src = a.M.q + (int64_t)row * a.M.ld;
-            const uint8_t *zeros = a.M.z + (int64_t)row * a.M.ng;
-            auto load = [&](int k, uint4 (&w)[4], uint32_t (&z)[GROUPS]) {
-#pragma unroll
-                for (int g = 0; g < GROUPS; ++g)
-                    z[g] = a.M.z ? __ldg(zeros + min(k * GROUPS + g, a.M.ng - 1)) : 8u;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    w[c] = k < k1 && k * 16 + 4 * c < a.M.ld
-                               ? __ldg(reinterpret_cast<const uint4 *>(src + k * 16 + 4 * c))
-                               : make_uint4(0, 0, 0, 0);
-            };
-            uint4 w[2][4];                       // this stage and the next
-            uint32_t zv[2][GROUPS];
-            load(k0, w[0], zv[0]);
-            load(k0 + 1, w[1], zv[1]);
-            for (int k = k0; k < k1 && ok; k += 2) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (k + i >= k1) break;
-                    uint32_t r[2][32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 v = w[i][2 * h + c / 4];
-                            const uint32_t x = c % 4 == 0 ? v.x : c % 4 == 1 ? v.y : c % 4 == 2 ? v.z : v.w;
-                            const ZeroPoint z = zero_point(zv[i][(8 * h + c) * 8 / GROUP] & 15u);
-                            r[h][4 * c] = code_pair0(x, z);
-                            r[h][4 * c + 1] = code_pair1(x, z);
-                            r[h][4 * c + 2] = code_pair0(x >> 8, z);
-                            r[h][4 * c + 3] = code_pair1(x >> 8, z);
-                        }
-                    load(k + i + 2, w[i], zv[i]);
-                    // a stage is handed over once the next one is decoded: its stores to TMEM
-                    // have had that time
-                    if (it > 0) hand_over((it - 1) % kRing);
-                    const uint32_t s = it % kRing;
-                    if (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane)) {
+    } else if (warp == 2 + kDrainWarps + kDecodeWarps) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+                int k0, k1;
+                stages_of(unit, k0, k1);
+                const int r0 = unit / a.parts / a.ntiles * BM;
+                for (int k = k0; k < k1; ++k, ++it) {
+                    const int s = it % CODES;
+                    if (it >= CODES && !mbar_wait(&c_empty[s], (it / CODES - 1) & 1, nullptr)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), r[h]);
-                    ++it;
+                    mbar_expect_tx(&c_full[s], kCodeBytes);
+                    tma_load_2d(codes + s * kCodeBytes, &maps.codes, k * (kStageK / 8), r0, &c_full[s]);
                 }
             }
         }
-        if (ok && it > 0) hand_over((it - 1) % kRing);
+    } else {
+        // decode: the warps of a quarter take its stages in turn
+        const int q = warp & 3, r = 32 * q + lane;
+        const uint32_t turn = (warp - 2 - kDrainWarps) / 4;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int unit = blockIdx.x; unit < a.units && ok; unit += gridDim.x) {
+            int k0, k1;
+            stages_of(unit, k0, k1);
+            const int row = min(unit / a.parts / a.ntiles * BM + r, a.m - 1);
+            const uint8_t *zeros = a.M.z + (int64_t)row * a.M.ng;
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k, ++it) {
+                if ((it & 1) != turn) continue;
+                uint32_t zv[GROUPS];
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g)
+                    zv[g] = a.M.z ? __ldg(zeros + min(k * GROUPS + g, a.M.ng - 1)) : 8u;
+                const uint32_t cs = it % CODES, s = it % kRing;
+                if (!warp_wait(&c_full[cs], it / CODES & 1, lane) ||
+                    (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // 16 words of the row, in chunks of 16 bytes that the copy permuted with it
+                const uint32_t base = smem_u32(codes + cs * kCodeBytes) + r * 64;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[8], v[32];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]),
+                                       "=r"(w[4 * c + 3])
+                                     : "r"(base + (((2 * h + c) ^ (r >> 1 & 3)) << 4)));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const ZeroPoint z = zero_point(zv[(8 * h + c) * 8 / GROUP] & 15u);
+                        v[4 * c] = code_pair0(w[c], z);
+                        v[4 * c + 1] = code_pair1(w[c], z);
+                        v[4 * c + 2] = code_pair0(w[c] >> 8, z);
+                        v[4 * c + 3] = code_pair1(w[c] >> 8, z);
+                    }
+                    tmem_st32(tmem_a + s * kStageA + 32 * h + ((uint32_t)(32 * q) << 16), v);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&c_empty[cs]);
+                    mbar_arrive(&full[s]);
+                }
+            }
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -408,6 +428,7 @@ cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *x
     for (int t = 0; t < terms; ++t)
         if (!make_map_bf16(&maps.x[t], xw + t * ldx, B, ldx, terms * ldx, p.BN))
             return cudaErrorInvalidValue;
+    if (!make_map_u32(&maps.codes, M.q, m, M.ld, kStageK / 8, BM)) return cudaErrorInvalidValue;
     TcArgs a;
     a.M = M;
     a.m = (int)m, a.B = (int)B;
