@@ -17,13 +17,13 @@ namespace w4 {
 // operations.
 //
 // The search runs in FP32 (six FMA-pipe operations a column and candidate: the clamp is the
-// saturation of an FMA in units of 15 steps) and is off by less than 2.7e-5 of E (16 roundings of
-// a term and of the sum, 1e-6; a column within 3.2e-6 steps of a half that rounds the other way,
-// 2.6e-5 of its term); a candidate within kNear of the best so far is settled in FP64, both of
+// saturation of an FMA in units of 15 steps) and is off by less than 4.5e-5 of E (16 roundings of
+// a term and of the sum, 1e-6; a column within 5.4e-6 steps of a half that rounds the other way,
+// 4.4e-5 of its term); a candidate within kNear of the best so far is settled in FP64, both of
 // them anew (about one comparison in 10000).
 // ---------------------------------------------------------------------------------
 constexpr int kPer = 16;            // columns per lane
-constexpr float kNear = 6e-5f;
+constexpr float kNear = 1e-4f;
 constexpr float kMagic = 12582912.f;   // 1.5 2^23: adding it leaves rint(x) in the low bits
 
 // rint(w / s) of the exact quotient, ties to even, exact for |w / s| <= 16 (larger
@@ -36,6 +36,13 @@ __device__ __forceinline__ float exact_rint(float w, float s, float inv) {
     if (rem > half || (rem == half && odd)) a += 1.f;
     if (rem < -half || (rem == -half && odd)) a -= 1.f;
     return a;
+}
+
+// 1 / x to a unit in the last place or so, for normal x.
+__device__ __forceinline__ float rcp(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // Maxima that hand on a NaN.
@@ -72,7 +79,7 @@ __device__ __forceinline__ void candidate(double alpha, float lo, float hi, bool
         const double x = -alpha * (double)lo, c = (double)s;
         double v;
         if (s > 0x1p-100f && s < 0x1p100f) {
-            const double r0 = (double)__frcp_rn(s);
+            const double r0 = (double)rcp(s);
             v = quotient(x, c, fma(fma(-c, r0, 1.0), r0, r0));
         } else {
             v = x / c;
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(256)
         for (int c0 = 0; c0 < grid; c0 += LPG) {
             float ms, mz;                               // lane ``sub`` forms candidate c0 + sub
             candidate(1.0 - (c0 + sub) / (2.0 * grid), lo, hi, zeros, ms, mz);
-            const float minv = 1.f / (15.f * ms);
+            const float minv = rcp(15.f * ms);
             for (int j = 0; j < min(LPG, grid - c0); ++j) {
                 const int from = (threadIdx.x & 31 & ~(LPG - 1)) | j;
                 const float cs = __shfl_sync(0xffffffffu, ms, from),
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(256)
         // half and goes to even); a = rint(t) from the low bits of + kMagic.  The remainder
         // w - a s is exact: beyond half a step t was off a half by less than its last bit, and
         // the lane settles its columns one by one.
-        const float inv = 1.f / s, z15 = z * (1.f / 15.f);
+        const float inv = rcp(s), z15 = z * (1.f / 15.f);
         float dev = 0.f;
         uint32_t acc[2] = {0, 0};
 #pragma unroll
