@@ -379,8 +379,13 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
  *   X [B][n] (dtype dt, row stride n), Y [B][m] float: device.
  * The integers q - z and the activations (BF16, or FP32 as three BF16 terms that sum to it
  * exactly) are multiplied exactly, summed in FP32 within a group, scaled in FP32 and summed
- * in FP32 over the groups in a fixed order: the result of a row of X does not depend on
- * the run.  An infinite or NaN activation reaches its own row of Y alone.  Enqueue only.
+ * in FP32 over the groups in an order fixed by the sizes: the same call gives the same bits
+ * (another B may take another path and differ in the last ones).  An infinite or NaN
+ * activation reaches its own row of Y alone; should a device-side wait of a many-row call run
+ * out, the rows of W^ of that tile are NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
+ * ones three each) run on warp-level MMAs that read the codes once; more on tcgen05 with the
+ * decoded codes as an operand in tensor memory.  The codes of zeros past 15 count by their
+ * low four bits.  Enqueue only.
  */
 nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,
                        int64_t n, int32_t group, const void *X, nq_dtype dt, int64_t B, float *Y,
@@ -406,9 +411,10 @@ size_t nq_moe_workspace_size(int64_t B, int64_t d, int64_t f, int32_t E, int32_t
  *     gate and f..2f-1 the up projection; down: E matrices of d x f.
  *   Y [B][d] float; ids [B][top_k] int32 and weights [B][top_k] float: the chosen experts by
  *     falling logit and their p, each may be NULL.  All device.
- * Logits are summed in FP64; products as in nq_w4_matmul; the activated rows are FP32.  One
- * token's result does not depend on the others of the call beyond the order of summation
- * over its experts, which is fixed (ascending).  Sizes: 1 <= d, f <= 65536,
+ * Logits are summed in FP64; products as in nq_w4_matmul; the activated rows are FP32; y is
+ * summed in the order of ids.  A token's result does not depend on the others of the call.
+ * Two launches: the logits, and one cooperative kernel for the rest (its grid-wide waits are
+ * bounded; should one run out, Y is NaN).  Sizes: 1 <= d, f <= 65536,
  * 1 <= top_k <= min(E, NQ_MOE_MAX_TOP_K), E <= NQ_MOE_MAX_EXPERTS, E 2f and E d <= 2^24
  * (NQ_ERR_INVALID_ARG otherwise).  Enqueue only.
  */

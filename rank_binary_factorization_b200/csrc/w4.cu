@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(256)
     range_of(w, zeros, lo, hi);
     hi = group_max<LPG>(hi);
     lo = -group_max<LPG>(-lo);
-    const bool nan = !(hi - lo < __int_as_float(0x7f800000));    // a weight that is not finite
+    // a weight that is not finite
+    const bool nan = !(hi < __int_as_float(0x7f800000)) || !(lo > __int_as_float(0xff800000));
 
     float s, z;
     if constexpr (!SEARCH) {

@@ -58,7 +58,8 @@ def test_quantize_settles_halves_and_extremes_as_the_exact_quotient(nq, symmetri
         row[:len(near)] = near
         row[-2], row[-1] = -7 * s, 7 * s
         rows += [row, np.abs(row), -np.abs(row)]
-    rows += [np.zeros(64), np.full(64, 2.0 ** -149), np.full(64, 3e38), -np.full(64, 1e-39)]
+    rows += [np.zeros(64), np.full(64, 2.0 ** -149), np.full(64, 3e38), -np.full(64, 1e-39),
+             3e38 * np.linspace(-1, 1, 64)]
     W = torch.from_numpy(np.array(rows)).float()
     for grid in (1, 5):
         for group in (32, 64):
@@ -246,6 +247,63 @@ def test_calls_on_another_stream_and_in_a_graph(nq):
                 static.copy_(X * k)
                 graph.replay()
                 assert torch.equal(out, ref * k)
+
+
+@pytest.mark.parametrize("B", [3, 40, 300])
+def test_calls_on_two_streams_at_once(nq, B):
+    What, (packed, scales, z) = layer(1000, 2048, 64, True, 23)
+    X = acts(B, 2048, torch.float32, 24).cuda()
+    ref = nq.nq_w4_matmul(packed, scales, X, group=64, zeros=z)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    out = []
+    for _ in range(8):
+        for s in streams:
+            with torch.cuda.stream(s):
+                out.append(nq.nq_w4_matmul(packed, scales, X, group=64, zeros=z))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for y in out)
+
+
+def test_long_axis_and_many_rows(nq):
+    # the longest k axis, on every path; more rows than one launch's worth of blocks
+    _check_product(nq, 40, 65536, 128, True, torch.bfloat16, 2, 51)
+    _check_product(nq, 40, 65536, 64, False, torch.bfloat16, 20, 52)
+    _check_product(nq, 70000, 64, 32, True, torch.float32, 1, 53)
+    _check_product(nq, 70000, 64, 32, False, torch.bfloat16, 33, 54)
+
+
+def test_repeated_calls_give_the_same_bits(nq):
+    What, (packed, scales, z) = layer(700, 3000, 128, True, 61)
+    for B in (1, 7, 16, 90):
+        for dtype in (torch.float32, torch.bfloat16):
+            X = acts(B, 3000, dtype, 62).cuda()
+            ref = nq.nq_w4_matmul(packed, scales, X, group=128, zeros=z)
+            for _ in range(5):
+                assert torch.equal(nq.nq_w4_matmul(packed, scales, X, group=128, zeros=z), ref)
+
+
+def test_zero_points_past_4_bits_count_by_their_low_bits(nq):
+    What, (packed, scales, z) = layer(60, 512, 64, True, 71)
+    X = acts(20, 512, torch.bfloat16, 72).cuda()
+    for x in (X[:2].contiguous(), X):
+        assert torch.equal(nq.nq_w4_matmul(packed, scales, x, group=64, zeros=z + 48),
+                           nq.nq_w4_matmul(packed, scales, x, group=64, zeros=z))
+    assert torch.equal(nq.nq_w4_dequantize(packed, scales, 512, 64, z + 48),
+                       nq.nq_w4_dequantize(packed, scales, 512, 64, z))
+
+
+def test_scales_that_start_off_a_word(nq):
+    # a row slice of a larger layer: scales and zero points at any address
+    What, (packed, scales, z) = layer(65, 768, 128, True, 81)
+    X = acts(30, 768, torch.float32, 82).cuda()
+    for x in (X[:1].contiguous(), X[:4].contiguous(), X):
+        ref = nq.nq_w4_matmul(packed, scales, x, group=128, zeros=z)
+        flat_s = torch.cat([scales.new_zeros(1), scales.flatten()])[1:].view(65, -1)
+        flat_z = torch.cat([z.new_zeros(1), z.flatten()])[1:].view(65, -1)
+        assert torch.equal(nq.nq_w4_matmul(packed, flat_s, x, group=128, zeros=flat_z), ref)
+        assert torch.equal(nq.nq_w4_matmul(packed[1:], scales[1:], x, group=128, zeros=z[1:]),
+                           ref[:, 1:])
 
 
 def test_from_calibration_to_a_quantised_layer(nq):
