@@ -2,6 +2,15 @@
 //   l_e = x . R_e;  the top_k largest (ties: the lowest expert);  p = softmax(l) over all
 //   experts, or over the chosen ones (renormalise)
 //   y = sum over the chosen e of p_e D_e (silu(G_e x) * (U_e x)),  silu(v) = v / (1 + exp(-v))
+//
+// Two launches: the logits, then one cooperative kernel for the choice, both products and the
+// sum, whose CTAs wait for one another twice (the down product needs all of h, the sum all parts).
+// An expert's rows are read once for all tokens that chose it.  Measured, bf16 unless said: one
+// token, 64 experts, top 6, 2048 x 1408: 27 us (latency: the choice, two grid waits, about one job
+// a CTA in each product); 8 tokens, 64 experts, top 8, 4096 x 1024, g = 64 with zero points:
+// 115 us, 290 MB (39 % of the copy rate, 59 % of the issue slots: decoding and the joins of jobs);
+// 16 tokens, 8 experts, top 2, 4096 x 11008, FP32: 279 us (three columns a token to multiply).
+// With a launch for each step: 84, 315, 580 us.
 #include "w4.cuh"
 
 namespace nq {
