@@ -51,6 +51,37 @@ __device__ __forceinline__ float rcp(float x) {
     return r;
 }
 
+// Two FP32 values in one operation each, rounded as apart: the FMA pipe takes as long, but half
+// the issue slots.
+struct Two {
+    uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 apart(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
 // Maxima that hand on a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float m;
@@ -195,16 +226,18 @@ __global__ void __launch_bounds__(256)
                             cz = __shfl_sync(0xffffffffu, mz, from),
                             inv = __shfl_sync(0xffffffffu, minv, from);
                 const float z15 = cz * (1.f / 15.f), off = kMagic + cz;
-                float e0 = 0.f, e1 = 0.f;
+                const Two m2 = two(kMagic, kMagic), n2 = two(-off, -off), s2 = two(-cs, -cs);
+                Two e2 = two(0.f, 0.f);
 #pragma unroll
                 for (int i = 0; i < kPer; i += 2) {
-                    const float v0 = fmaf(__saturatef(fmaf(w[i], inv, z15)), 15.f, kMagic) - off,
-                                v1 = fmaf(__saturatef(fmaf(w[i + 1], inv, z15)), 15.f, kMagic) - off;
-                    const float t0 = fmaf(-cs, v0, w[i]) * d[i], t1 = fmaf(-cs, v1, w[i + 1]) * d[i + 1];
-                    e0 = fmaf(t0, t0, e0);
-                    e1 = fmaf(t1, t1, e1);
+                    const Two u = two(__saturatef(fmaf(w[i], inv, z15)),
+                                      __saturatef(fmaf(w[i + 1], inv, z15)));
+                    const Two v = add2(fma2(u, two(15.f, 15.f), m2), n2);
+                    const Two t = mul2(fma2(s2, v, two(w[i], w[i + 1])), two(d[i], d[i + 1]));
+                    e2 = fma2(t, t, e2);
                 }
-                const float e = group_sum<LPG>(e0 + e1);
+                const float2 ea = apart(e2);
+                const float e = group_sum<LPG>(ea.x + ea.y);
                 const bool first = c0 + j == 0;
                 const bool safe = plain && e > 1e-30f && best > 1e-30f && best < 1e30f;
                 bool less = first || (safe && e < best * (1.f - kNear));
@@ -236,16 +269,23 @@ __global__ void __launch_bounds__(256)
         // w - a s is exact: beyond half a step t was off a half by less than its last bit, and
         // the lane settles its columns one by one.
         const float inv = rcp(s), z15 = z * (1.f / 15.f);
+        const Two i2 = two(inv, inv), s2 = two(-s, -s), m2 = two(kMagic, kMagic);
         float dev = 0.f;
         uint32_t acc[2] = {0, 0};
 #pragma unroll
-        for (int i = kPer - 1; i >= 0; --i) {
-            const float t0 = w[i] * inv, t = fmaf(fmaf(-t0, s, w[i]), inv, t0);
-            const float a = (t + kMagic) - kMagic;
-            dev = fmaxf(dev, fabsf(fmaf(-a, s, w[i])));
+        for (int i = kPer - 2; i >= 0; i -= 2) {
+            const Two w2 = two(w[i], w[i + 1]);
+            const Two t0 = mul2(w2, i2);
+            const Two t = fma2(fma2(t0, s2, w2), i2, t0);
+            const Two a2 = add2(add2(t, m2), two(-kMagic, -kMagic));
+            const float2 rem = apart(fma2(a2, s2, w2)), a = apart(a2);
+            dev = fmaxf(dev, fmaxf(fabsf(rem.x), fabsf(rem.y)));
             // clamped to 0 .. 15 in units of 15, and back
-            const float c = fmaf(__saturatef(fmaf(a, 1.f / 15.f, z15)), 15.f, kMagic);
-            acc[i / 8] = acc[i / 8] * 16u + __float_as_uint(c);
+            const float2 c = apart(fma2(two(__saturatef(fmaf(a.x, 1.f / 15.f, z15)),
+                                            __saturatef(fmaf(a.y, 1.f / 15.f, z15))),
+                                        two(15.f, 15.f), m2));
+            acc[i / 8] = acc[i / 8] * 16u + __float_as_uint(c.y);
+            acc[i / 8] = acc[i / 8] * 16u + __float_as_uint(c.x);
         }
         // the eight codes carry the bits of kMagic each
         word[0] = acc[0] - 0x4b400000u * 0x11111111u;
