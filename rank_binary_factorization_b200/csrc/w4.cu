@@ -28,7 +28,8 @@ namespace w4 {
 // 50 % of the copy rate, 82 % of the issue slots (16 rounded quotients a lane); the correction of
 // the quotient instead of a settled remainder for every column: 614 -> 190 us.
 // ---------------------------------------------------------------------------------
-constexpr int kPer = 16;            // columns per lane
+constexpr int kPer = 16;            // columns per lane (kWide: BF16 without a search)
+constexpr int kWide = 32;
 constexpr float kNear = 1e-4f;
 constexpr float kMagic = 12582912.f;   // 1.5 2^23: adding it leaves rint(x) in the low bits
 
@@ -149,40 +150,41 @@ __device__ __forceinline__ double exact_error(const float (&w)[kPer], const floa
     return e;
 }
 
-template <typename T>
-__device__ __forceinline__ void load_per(const T *src, int k0, int n, bool vec, float (&v)[kPer]) {
-    if (vec && k0 + kPer <= n) {
-        constexpr int NV = kPer * sizeof(T) / 16;
+template <int PER, typename T>
+__device__ __forceinline__ void load_per(const T *src, int k0, int n, bool vec, float (&v)[PER]) {
+    if (vec && k0 + PER <= n) {
+        constexpr int NV = PER * sizeof(T) / 16;
         uint4 raw[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) raw[i] = __ldg(reinterpret_cast<const uint4 *>(src + k0) + i);
         const T *h = reinterpret_cast<const T *>(raw);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = (float)h[i];
+        for (int i = 0; i < PER; ++i) v[i] = (float)h[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = k0 + i < n ? (float)src[k0 + i] : 0.f;
+        for (int i = 0; i < PER; ++i) v[i] = k0 + i < n ? (float)src[k0 + i] : 0.f;
     }
 }
 
 // lo = min(0, min w) and hi = max(0, max w) (without zeros: hi = max |w|); NaN in hi if in w.
-__device__ __forceinline__ void range_of(const float (&w)[kPer], bool zeros, float &lo, float &hi) {
+template <int PER>
+__device__ __forceinline__ void range_of(const float (&w)[PER], bool zeros, float &lo, float &hi) {
     lo = hi = 0.f;
     if (zeros) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < PER; ++i) {
             lo = fminf(lo, w[i]);
             hi = max_nan(hi, w[i]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) hi = max_nan(hi, fabsf(w[i]));
+        for (int i = 0; i < PER; ++i) hi = max_nan(hi, fabsf(w[i]));
     }
 }
 
 // A row is worked on by 2^ltpr lanes (LPG to a group) side by side, blockIdx.y of them after one
 // another along the row.
-template <int LPG, bool SEARCH, typename T>
+template <int PER, int LPG, bool SEARCH, typename T>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const T *__restrict__ W, int64_t m, int n, const float *__restrict__ d_in,
                     int grid, int vec, int dvec, int ltpr, int ld, int ng, uint32_t *__restrict__ q,
@@ -190,9 +192,9 @@ __global__ void __launch_bounds__(256)
     const int64_t row = ((int64_t)blockIdx.x << (8 - ltpr)) + (threadIdx.x >> ltpr);
     const int u = ((int)blockIdx.y << ltpr) + (threadIdx.x & ((1 << ltpr) - 1));
     const bool live = row < m && u < ng * LPG;          // whole groups
-    const int k0 = u * kPer;
+    const int k0 = u * PER;
     const bool zeros = zp != nullptr;
-    float w[kPer], lo, hi;
+    float w[PER], lo, hi;
     load_per(W + (live ? row * n : 0), live ? k0 : n, n, vec, w);
     range_of(w, zeros, lo, hi);
     hi = group_max<LPG>(hi);
@@ -204,12 +206,12 @@ __global__ void __launch_bounds__(256)
     if constexpr (!SEARCH) {
         candidate(1.0, lo, hi, zeros, s, z);
     } else {
-        float d[kPer];
+        float d[PER];
         if (d_in) {
             load_per(d_in, live ? k0 : n, n, dvec, d);
         } else {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) d[i] = 1.f;
+            for (int i = 0; i < PER; ++i) d[i] = 1.f;
         }
         // outside this range of weights and errors every candidate is settled in FP64
         const bool plain = hi - lo > 1e-25f && hi - lo < 1e25f;
@@ -229,7 +231,7 @@ __global__ void __launch_bounds__(256)
                 const Two m2 = two(kMagic, kMagic), n2 = two(-off, -off), s2 = two(-cs, -cs);
                 Two e2 = two(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < kPer; i += 2) {
+                for (int i = 0; i < PER; i += 2) {
                     const Two u = two(__saturatef(fmaf(w[i], inv, z15)),
                                       __saturatef(fmaf(w[i + 1], inv, z15)));
                     const Two v = add2(fma2(u, two(15.f, 15.f), m2), n2);
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(256)
     }
     // a group with a weight that is not finite reads back as NaN
     if (nan) s = __int_as_float(0x7fc00000), z = zeros ? 0.f : 8.f;
-    uint32_t word[2];
+    uint32_t word[PER / 8];
     {
         // t = w / s, rounded correctly (quotient and one correction, so a half comes out as the
         // half and goes to even); a = rint(t) from the low bits of + kMagic.  The remainder
@@ -271,9 +273,9 @@ __global__ void __launch_bounds__(256)
         const float inv = rcp(s), z15 = z * (1.f / 15.f);
         const Two i2 = two(inv, inv), s2 = two(-s, -s), m2 = two(kMagic, kMagic);
         float dev = 0.f;
-        uint32_t acc[2] = {0, 0};
+        uint32_t acc[PER / 8] = {};
 #pragma unroll
-        for (int i = kPer - 2; i >= 0; i -= 2) {
+        for (int i = PER - 2; i >= 0; i -= 2) {
             const Two w2 = two(w[i], w[i + 1]);
             const Two t0 = mul2(w2, i2);
             const Two t = fma2(fma2(t0, s2, w2), i2, t0);
@@ -288,31 +290,40 @@ __global__ void __launch_bounds__(256)
             acc[i / 8] = acc[i / 8] * 16u + __float_as_uint(c.x);
         }
         // the eight codes carry the bits of kMagic each
-        word[0] = acc[0] - 0x4b400000u * 0x11111111u;
-        word[1] = acc[1] - 0x4b400000u * 0x11111111u;
+#pragma unroll
+        for (int i = 0; i < PER / 8; ++i) word[i] = acc[i] - 0x4b400000u * 0x11111111u;
         // (also where s is 0, NaN, or so small that 1 / s or a remainder is not exact)
         if (!(s > 0x1p-100f) || !(dev <= 0.5f * s)) {
             const float up = scale_up(s);
-            word[0] = word[1] = 0;
 #pragma unroll 1
-            for (int i = 0; i < kPer; ++i) {
+            for (int i = 0; i < PER; ++i) {
                 float wi = 0.f;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j)
+                for (int j = 0; j < PER; ++j)
                     if (j == i) wi = w[j];
-                const float v = exact_code(wi, s, z, up);
-                word[i >> 3] |= (uint32_t)(int)(v + z) << (4 * (i & 7));
+                const uint32_t c = (uint32_t)(int)(exact_code(wi, s, z, up) + z);
+#pragma unroll
+                for (int j = 0; j < PER / 8; ++j)
+                    if (j == i >> 3) word[j] = i & 7 ? word[j] | c << (4 * (i & 7)) : c;
             }
         }
     }
     if (!live) return;
-    if (k0 + kPer > n) {                                // codes past the last column are 0
-        const int left = n - k0;
-        word[0] = left <= 0 ? 0 : left < 8 ? word[0] & ((1u << 4 * left) - 1) : word[0];
-        word[1] = left <= 8 ? 0 : word[1] & ((1u << 4 * (left - 8)) - 1);
+    if (k0 + PER > n) {                                // codes past the last column are 0
+#pragma unroll
+        for (int i = 0; i < PER / 8; ++i) {
+            const int left = n - k0 - 8 * i;
+            word[i] = left <= 0 ? 0 : left < 8 ? word[i] & ((1u << 4 * left) - 1) : word[i];
+        }
     }
-    const int wi = u * 2;
-    if (wi < ld) *reinterpret_cast<uint2 *>(q + row * ld + wi) = make_uint2(word[0], word[1]);
+    const int wi = u * (PER / 8);
+    if (wi < ld) {                                      // (ld is a multiple of 4)
+        uint32_t *dst = q + row * ld + wi;
+        if constexpr (PER == 32)
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
+        else
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(word[0], word[1]);
+    }
     if (u % LPG == 0) {
         const int64_t at = row * ng + u / LPG;
         sc[at] = __float2bfloat16_rn(s);
@@ -327,35 +338,35 @@ static int row_lanes(int64_t units, int least) {
     return l;
 }
 
-template <int LPG>
-static cudaError_t quantize_t(const void *W, int w_bf16, int64_t m, int64_t n, const float *d_in,
-                              int group, int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z,
-                              cudaStream_t st) {
-    const int ld = (int)row_words(n), ng = (int)row_groups(n, group);
-    const int ltpr = row_lanes(ng * LPG, LPG == 8 ? 3 : LPG == 4 ? 2 : 1);
-    const dim3 blocks((unsigned)ceil_div(m, 256 >> ltpr), (unsigned)ceil_div(ng * LPG, 1 << ltpr));
-    const int vec = n % (w_bf16 ? 8 : 4) == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
+// W by lanes of PER columns; a search takes kPer.
+template <int PER, bool SEARCH, typename T>
+static void quantize_launch(const T *W, int64_t m, int64_t n, const float *d_in, int group, int grid,
+                            uint32_t *q, __nv_bfloat16 *s, uint8_t *z, cudaStream_t st) {
+    const int ld = (int)row_words(n), ng = (int)row_groups(n, group), lpg = group / PER;
+    const int ltpr = row_lanes(ng * lpg, lpg == 8 ? 3 : lpg == 4 ? 2 : lpg == 2 ? 1 : 0);
+    const dim3 blocks((unsigned)ceil_div(m, 256 >> ltpr), (unsigned)ceil_div(ng * lpg, 1 << ltpr));
+    const int vec = n % (16 / sizeof(T)) == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0;
     const int dvec = reinterpret_cast<uintptr_t>(d_in) % 16 == 0;
-    auto run = [&](auto kern, auto *src) {
-        kern<<<blocks, 256, 0, st>>>(src, m, (int)n, d_in, grid, vec, dvec, ltpr, ld, ng, q, s, z);
-    };
-    const __nv_bfloat16 *wb = static_cast<const __nv_bfloat16 *>(W);
-    const float *wf = static_cast<const float *>(W);
-    if (w_bf16)
-        grid > 1 ? run(quantize_kernel<LPG, true, __nv_bfloat16>, wb)
-                 : run(quantize_kernel<LPG, false, __nv_bfloat16>, wb);
-    else
-        grid > 1 ? run(quantize_kernel<LPG, true, float>, wf)
-                 : run(quantize_kernel<LPG, false, float>, wf);
+    auto kern = group == 32   ? quantize_kernel<PER, 32 / PER, SEARCH, T>
+                : group == 64 ? quantize_kernel<PER, 64 / PER, SEARCH, T>
+                              : quantize_kernel<PER, 128 / PER, SEARCH, T>;
+    kern<<<blocks, 256, 0, st>>>(W, m, (int)n, d_in, grid, vec, dvec, ltpr, ld, ng, q, s, z);
     count_launch();
-    return cudaGetLastError();
 }
 
 cudaError_t quantize(const void *W, int w_bf16, int64_t m, int64_t n, const float *d_in, int group,
                      int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z, cudaStream_t st) {
-    if (group == 32) return quantize_t<2>(W, w_bf16, m, n, d_in, group, grid, q, s, z, st);
-    if (group == 64) return quantize_t<4>(W, w_bf16, m, n, d_in, group, grid, q, s, z, st);
-    return quantize_t<8>(W, w_bf16, m, n, d_in, group, grid, q, s, z, st);
+    const __nv_bfloat16 *wb = static_cast<const __nv_bfloat16 *>(W);
+    const float *wf = static_cast<const float *>(W);
+    // BF16 without a search: the scale's arithmetic bounds it, shared by twice the columns in a
+    // lane; FP32 is bound by memory, and 128 bytes a lane would be by the loads.
+    if (w_bf16)
+        grid > 1 ? quantize_launch<kPer, true>(wb, m, n, d_in, group, grid, q, s, z, st)
+                 : quantize_launch<kWide, false>(wb, m, n, d_in, group, grid, q, s, z, st);
+    else
+        grid > 1 ? quantize_launch<kPer, true>(wf, m, n, d_in, group, grid, q, s, z, st)
+                 : quantize_launch<kPer, false>(wf, m, n, d_in, group, grid, q, s, z, st);
+    return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------------
