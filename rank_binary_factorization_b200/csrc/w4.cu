@@ -22,11 +22,12 @@ namespace w4 {
 // 4.4e-5 of its term); a candidate within kNear of the best so far is settled in FP64, both of
 // them anew (about one comparison in 10000).
 //
-// Measured: 4096x4096 BF16, g = 128, 16 candidates 127 us, three times the 44 us that the search's
-// FMA-pipe operations take at full rate: issue (shuffles, sums across a group's lanes,
-// the settled pairs) bounds it.  28672x8192 BF16, g = 64, zero points, one candidate: 184 us, 598 MB,
-// 50 % of the copy rate, 82 % of the issue slots (16 rounded quotients a lane); the correction of
-// the quotient instead of a settled remainder for every column: 614 -> 190 us.
+// Measured: 4096x4096 BF16, g = 128, 16 candidates 93 us, twice the 44 us that the search's FMA-pipe
+// operations take at full rate: latency and issue (shuffles, sums across a group's lanes, the settled
+// pairs) bound it.  28672x8192 BF16, g = 64, zero points, one candidate: 137 us, 598 MB, 68 % of the
+// copy rate, bound by issue (a rounded quotient for every column); FP32, g = 32: 186 us, 90 %, bound by
+// memory.  The correction of the quotient instead of a settled remainder for every column:
+// 614 -> 190 us; two columns an operation and 32 a lane: 184 -> 137 us.
 // ---------------------------------------------------------------------------------
 constexpr int kPer = 16;            // columns per lane (kWide: BF16 without a search)
 constexpr int kWide = 32;
@@ -137,14 +138,18 @@ __device__ __forceinline__ float exact_code(float w, float s, float z, float up)
     return s > 0.f ? fminf(fmaxf(exact_rint(w * up, su, 1.f / su), -z), 15.f - z) : 0.f;
 }
 
-// The lane's part of E in FP64.
+// The lane's part of E in FP64.  Rare, so its columns go through local memory in a loop that leaves
+// the registers to the search (two CTAs an SM with it unrolled, four so: 116 -> 93 us).
 __device__ __forceinline__ double exact_error(const float (&w)[kPer], const float (&d)[kPer], float s,
                                            float z) {
+    float wl[kPer], dl[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) wl[i] = w[i], dl[i] = d[i];
     const float up = scale_up(s);
     double e = 0.0;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < kPer; ++i) {
-        const double t = ((double)w[i] - (double)s * (double)exact_code(w[i], s, z, up)) * (double)d[i];
+        const double t = ((double)wl[i] - (double)s * (double)exact_code(wl[i], s, z, up)) * (double)dl[i];
         e += t * t;
     }
     return e;
@@ -185,7 +190,7 @@ __device__ __forceinline__ void range_of(const float (&w)[PER], bool zeros, floa
 // A row is worked on by 2^ltpr lanes (LPG to a group) side by side, blockIdx.y of them after one
 // another along the row.
 template <int PER, int LPG, bool SEARCH, typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, SEARCH ? 4 : PER == 32 ? 4 : 5)
     quantize_kernel(const T *__restrict__ W, int64_t m, int n, const float *__restrict__ d_in,
                     int grid, int vec, int dvec, int ltpr, int ld, int ng, uint32_t *__restrict__ q,
                     __nv_bfloat16 *__restrict__ sc, uint8_t *__restrict__ zp) {

@@ -92,6 +92,31 @@ def test_a_weight_that_is_not_finite_spoils_its_own_group_only(nq, symmetric):
     assert torch.equal(out, ref)
 
 
+@pytest.mark.parametrize("symmetric", [True, False])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_one_candidate_of_bf16_weights(nq, group, symmetric):
+    # halves of a step, the type's extremes, zeros, subnormals; rows that end inside a word, a group
+    # and a lane's columns; an infinite or NaN weight spoils its own group only
+    rng = np.random.default_rng(group)
+    step, n = 2.0 ** -4, 203
+    halves = rng.choice(np.arange(-7, 7) + 0.5, size=n) * step
+    halves[::8] = 7 * step
+    rows = [halves, np.abs(halves), -np.abs(halves), np.zeros(n), np.full(n, 2.0 ** -133),
+            3.3e38 * np.linspace(-1, 1, n), rng.standard_normal(n)]
+    W = torch.from_numpy(np.array(rows)).to(torch.bfloat16)
+    _check_quantized(nq, W, group, None, symmetric, 1)
+    clean = nq.nq_w4_quantize(W.cuda(), group=group, symmetric=symmetric)
+    ref = nq.nq_w4_dequantize(clean["packed"], clean["scales"], n, group, clean["zeros"]).cpu()
+    for value in (float("nan"), float("inf"), float("-inf")):
+        bad = W.clone()
+        bad[6, 40] = value
+        q = nq.nq_w4_quantize(bad.cuda(), group=group, symmetric=symmetric)
+        out = nq.nq_w4_dequantize(q["packed"], q["scales"], n, group, q["zeros"]).cpu()
+        hit = torch.zeros_like(out, dtype=torch.bool)
+        hit[6, 40 // group * group:min(n, (40 // group + 1) * group)] = True
+        assert out[hit].isnan().all() and torch.equal(out[~hit], ref[~hit])
+
+
 def test_quantize_of_a_view_that_starts_off_a_16_byte_boundary(nq):
     rng = np.random.default_rng(6)
     flat = torch.from_numpy(rng.standard_normal(1 + 5 * 64)).to(torch.bfloat16).cuda()
