@@ -339,7 +339,7 @@ struct GateUpProb : ExpertJobs {
 template <int NT>
 struct DownProb : ExpertJobs {
     Red<1, NT> *red;
-    bool ok = true;                        // all of h was there
+    bool ok = true;                        // all of h was there (else its parts are NaN)
     __device__ DownProb(const MoeArgs &a, const Lists &L, int per, Red<1, NT> *red_)
         : ExpertJobs(a, L, a.f, a.d, kTerms, per), red(red_) {}
     __device__ __forceinline__ int first_row(const Cursor &c, int wr, int) const {
@@ -366,7 +366,8 @@ struct DownProb : ExpertJobs {
         for (int o = threadIdx.x - wr * 32 * WK; o < 16 * np; o += 32 * WK) {
             const int r = o % 16, p = o / 16;
             if (r0 + r < a.d)
-                a.part[(int64_t)L.pairs[p0 + p] * a.d + r0 + r] = R.sum(wr, WK, r, p * kTerms, kTerms);
+                a.part[(int64_t)L.pairs[p0 + p] * a.d + r0 + r] =
+                    ok ? R.sum(wr, WK, r, p * kTerms, kTerms) : __int_as_float(0x7fc00000);
         }
     }
 };
