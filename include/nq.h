@@ -377,10 +377,10 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
 /*
  * Y = X W^^T:  Y[b][i] = sum_k W^[i][k] X[b][k] for B <= 65536 rows of X.
  *   X [B][n] (dtype dt, row stride n), Y [B][m] float: device.
- * The integers q - z and the activations (BF16, or FP32 as three BF16 terms that sum to it
- * exactly) are multiplied exactly, summed in FP32 within a group, scaled in FP32 and summed
- * in FP32 over the groups in an order fixed by the sizes: the same call gives the same bits
- * (another B may take another path and differ in the last ones).  An infinite or NaN
+ * The integers q - z and the activations (BF16, or FP32 as three BF16 terms that sum to it,
+ * exactly from 2^-110 on) are multiplied exactly, summed in FP32 within a group, scaled in
+ * FP32 and summed in FP32 over the groups in an order fixed by the sizes: the same call gives
+ * the same bits (another B may take another path and differ in the last ones).  An infinite or NaN
  * activation reaches its own row of Y alone; should a device-side wait of a many-row call run
  * out, the rows of W^ of that tile are NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
  * ones three each) run on warp-level MMAs that read the codes once; more on tcgen05 with the
