@@ -380,8 +380,11 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
  * The integers q - z and the activations (BF16, or FP32 as three BF16 terms that sum to it,
  * exactly from 2^-110 on) are multiplied exactly, summed in FP32 within a group, scaled in
  * FP32 and summed in FP32 over the groups in an order fixed by the sizes: the same call gives
- * the same bits (another B may take another path and differ in the last ones).  An infinite or NaN
- * activation reaches its own row of Y alone; should a device-side wait of a many-row call run
+ * the same bits (another B may take another path and differ in the last ones).  Sums are
+ * carried in units of 2^11, so that no product or group's sum of finite activations overflows, nor
+ * any other sum whose value is in range; results below 2^-115 are rounded to multiples of 2^-138.
+ * An infinite or NaN activation reaches its own row of Y
+ * alone, a scale that is not finite its own column; should a device-side wait of a many-row call run
  * out, the rows of W^ of that tile are NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
  * ones three each) run on warp-level MMAs that read the codes once; more on tcgen05 with the
  * decoded codes as an operand in tensor memory.  The codes of zeros past 15 count by their

@@ -41,19 +41,23 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 of a word as the BF16 pair ((q_i - z) / 4, (q_{i+4} - z) / 4), exactly, for
-// i = 0, 1 (i = 2, 3: the word shifted right by 8).  Bits 0..3 of a half: the low mantissa
+// Codes i and i + 4 of a word as the BF16 pair ((q_i - z) / 2048, (q_{i+4} - z) / 2048), exactly,
+// for i = 0, 1 (i = 2, 3: the word shifted right by 8).  Bits 0..3 of a half: the low mantissa
 // bits of 128.0 (ulp 1) make 128 + q.  Bits 4..7 of a half alone are the BF16 number
-// q 2^-129 for every q (subnormals and the first binade are one line), which 2^127 brings to
-// q / 4.  So four pairs cost one shift, four logical operations and four FMAs.
+// q 2^-129 for every q (subnormals and the first binade are one line), which 2^118 brings to
+// q / 2048.  So four pairs cost one shift, four logical operations and four FMAs.
+// The unit of 1 / 2048 costs nothing and keeps the sums in range: 128 (the longest group) x 15 / 2048
+// is below 1, so no product and no group's sum of finite activations overflows, and the sum of
+// the groups does so only where the result itself is near the range's end.  At the other end, sums
+// below 2^-126 in this unit (results below 2^-115) lose their last bits.
 struct ZeroPoint {
-    uint32_t lo, hi;      // -(128 + z) / 4 and -z / 4, twice each
+    uint32_t lo, hi;      // -(128 + z) / 2048 and -z / 2048, twice each
 };
-// -32 has ulp 1/4: its low mantissa bits make -(32 + z / 4).
+// -1/16 has ulp 1/2048: its low mantissa bits make -(128 + z) / 2048.
 __device__ __forceinline__ ZeroPoint zero_point(uint32_t z) {
-    const uint32_t lo = (0xc200u | z) * 0x10001u, c32 = 0x42004200u;
+    const uint32_t lo = (0xbd80u | z) * 0x10001u, c16 = 0x3d803d80u;
     const __nv_bfloat162 hi = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&lo),
-                                      *reinterpret_cast<const __nv_bfloat162 *>(&c32));
+                                      *reinterpret_cast<const __nv_bfloat162 *>(&c16));
     return {lo, *reinterpret_cast<const uint32_t *>(&hi)};
 }
 __device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t b, uint32_t c) {
@@ -62,12 +66,12 @@ __device__ __forceinline__ uint32_t fma_pair(uint32_t a, uint32_t b, uint32_t c)
     return d;
 }
 __device__ __forceinline__ uint32_t code_pair0(uint32_t w, const ZeroPoint &z) {
-    return fma_pair((w & 0x000f000fu) | 0x43004300u, 0x3e803e80u /* 1/4 */, z.lo);
+    return fma_pair((w & 0x000f000fu) | 0x43004300u, 0x3a003a00u /* 1/2048 */, z.lo);
 }
 __device__ __forceinline__ uint32_t code_pair1(uint32_t w, const ZeroPoint &z) {
-    return fma_pair(w & 0x00f000f0u, 0x7f007f00u /* 2^127 */, z.hi);
+    return fma_pair(w & 0x00f000f0u, 0x7a807a80u /* 2^118 */, z.hi);
 }
-constexpr float kCodeUnit = 4.f;   // the pairs hold codes in units of 1/4
+constexpr float kCodeUnit = 2048.f;   // the pairs hold codes in units of 1/2048
 
 // 16 bytes global -> shared, asynchronously; zeros where ``in`` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool in) {

@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-// Y = sum over the parts, in their order.
+// Y = sum over the parts, in their order (in the unit of the codes until then, which keeps them in
+// range where Y is).
 __global__ void __launch_bounds__(256)
     w4_sum_parts_kernel(const float *__restrict__ part, int parts, int64_t count,
                         float *__restrict__ Y) {
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(256)
          i += (int64_t)gridDim.x * blockDim.x) {
         float v = 0.f;
         for (int p = 0; p < parts; ++p) v += part[p * count + i];
-        Y[i] = v;
+        Y[i] = kCodeUnit * v;
     }
 }
 
@@ -441,7 +442,7 @@ cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *x
     a.ntiles = (int)ceil_div(B, p.BN);
     a.units = (int)ceil_div(m, BM) * a.ntiles * p.parts;
     a.out = p.parts > 1 ? partial : Y;
-    a.out_scale = kCodeUnit;
+    a.out_scale = p.parts > 1 ? 1.f : kCodeUnit;
     cudaError_t e;
     if (terms == 1)
         e = p.BN == 32    ? tc_launch<32, 1>(maps, a, group, st)
