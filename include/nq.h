@@ -385,7 +385,7 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
  * any other sum whose value is in range; results below 2^-115 are rounded to multiples of 2^-138.
  * An infinite or NaN activation reaches its own row of Y
  * alone, a scale that is not finite its own column; should a device-side wait of a many-row call run
- * out, the rows of W^ of that tile are NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
+ * out, what it kept from being computed is NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
  * ones three each) run on warp-level MMAs that read the codes once; more on tcgen05 with the
  * decoded codes as an operand in tensor memory.  The codes of zeros past 15 count by their
  * low four bits.  Enqueue only.
@@ -556,6 +556,11 @@ size_t nq_selftest_workspace_size(void);
  * first.  Returns the device status the run raised (NQ_OK if none), NQ_ERR_INVALID_ARG /
  * NQ_ERR_WORKSPACE for bad arguments, NQ_ERR_UNSUPPORTED off sm_100.  Synchronises. */
 nq_status nq_selftest(int32_t kind, void *ws, size_t ws_bytes, nq_stream_t stream);
+
+/* Polls after which a device-side wait of nq_w4_matmul and nq_moe_w4 gives up (process-wide; at
+ * most, and by default or for -1, the library's own limit of many seconds).  With a few polls, or
+ * 0, a test sees what such a call leaves: it ends, and what its waits did not reach is NaN. */
+nq_status nq_set_w4_wait_polls(int32_t polls);
 
 #ifdef __cplusplus
 }

@@ -25,7 +25,7 @@ __all__ = [
     "nq_recon_error", "nq_pack_signs", "nq_binary_matmul", "nq_ls_refit", "LBState", "NQError",
     "status_string", "lib", "nq_w4_quantize", "nq_w4_dequantize", "nq_w4_matmul", "nq_moe_w4",
     "nq_launch_count", "nq_profile_enable", "nq_profile_get", "nq_selftest",
-    "nq_set_inverse_mode", "nq_set_tuning", "nq_set_latent_solver",
+    "nq_set_inverse_mode", "nq_set_tuning", "nq_set_latent_solver", "nq_set_w4_wait_polls",
 ]
 
 
@@ -343,6 +343,12 @@ def nq_set_tuning(key, value):
     """Scheduling setting ("factor_ctas", "newton_bn", "svid_beside", "nfast", "rhs_bn",
     "solve_bn", "newton_fused"; see nq_tuning)."""
     check("nq_set_tuning", lib.nq_set_tuning(_lib.TUNING[key], int(value)))
+
+
+def nq_set_w4_wait_polls(polls=-1):
+    """Polls after which a device-side wait of nq_w4_matmul and nq_moe_w4 gives up and leaves NaN
+    (process-wide, for tests of that path; -1: the library's own limit)."""
+    check("nq_set_w4_wait_polls", lib.nq_set_w4_wait_polls(int(polls)))
 
 
 def nq_launch_count():

@@ -1496,6 +1496,7 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     a.gate_up = w4_mat(gate_up, gate_up_scales, gate_up_zeros, d, group);
     a.down = w4_mat(down, down_scales, down_zeros, f, group);
     a.group = group;
+    a.polls = w4::wait_polls(kGridSpinLimit);
     a.Y = Y;
     a.ids = ids;
     a.weights = weights;
@@ -1506,6 +1507,12 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     a.part = at<float>(ws, L.part);
     ProfScope ps(NQ_K_MOE, cs(stream));
     NQ_CK(w4::moe(a, cs(stream)));
+    return NQ_OK;
+}
+
+nq_status nq_set_w4_wait_polls(int32_t polls) {
+    if (polls < -1) return NQ_ERR_INVALID_ARG;
+    w4::set_wait_polls(polls);
     return NQ_OK;
 }
 

@@ -235,9 +235,9 @@ __device__ __forceinline__ void arrive(unsigned int *bar) {
     __syncthreads();
     if (threadIdx.x == 0) release_add(bar, 1);
 }
-__device__ __forceinline__ bool all_arrived(unsigned int *bar) {
+__device__ __forceinline__ bool all_arrived(unsigned int *bar, uint32_t polls) {
     bool ok = true;
-    if (threadIdx.x == 0) ok = wait_geq(bar, gridDim.x, kGridSpinLimit);
+    if (threadIdx.x == 0) ok = wait_geq(bar, gridDim.x, polls);
     return __syncthreads_and(ok);
 }
 
@@ -349,7 +349,7 @@ struct DownProb : ExpertJobs {
         return (expert(c) + 1) * a.d - 1;
     }
     // the first copies of the weights are under way; h is complete when all CTAs have arrived
-    __device__ __forceinline__ void ready() { ok = all_arrived(a.bar); }
+    __device__ __forceinline__ void ready() { ok = all_arrived(a.bar, a.polls); }
     __device__ __forceinline__ const char *col(const Cursor &cur, int j, bool &odd) const {
         int pair, term;
         column(cur, j, pair, term);
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     }
     __threadfence();
     arrive(a.bar + 1);
-    ok = all_arrived(a.bar + 1) && ok;
+    ok = all_arrived(a.bar + 1, a.polls) && ok;
     const int64_t count = (int64_t)a.B * a.d;
     for (int64_t o = (int64_t)blockIdx.x * 32 * kWarps + threadIdx.x; o < count;
          o += (int64_t)gridDim.x * 32 * kWarps) {

@@ -23,9 +23,10 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
 }
 
 // Bounded wait for the completion of the phase with parity ``parity``.
-__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *err) {
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *err,
+                                          uint32_t polls = kMbarSpinLimit) {
     const uint32_t addr = smem_u32(bar);
-    for (uint32_t spin = 0; spin < kMbarSpinLimit; ++spin) {
+    for (uint32_t spin = 0; spin < polls; ++spin) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"

@@ -4,6 +4,13 @@
 namespace nq {
 namespace w4 {
 
+static std::atomic<int> g_wait_polls{-1};
+uint32_t wait_polls(uint32_t most) {
+    const int p = g_wait_polls.load(std::memory_order_relaxed);
+    return p < 0 || (uint32_t)p > most ? most : (uint32_t)p;
+}
+void set_wait_polls(int polls) { g_wait_polls.store(polls, std::memory_order_relaxed); }
+
 // ---------------------------------------------------------------------------------
 // Quantiser.  Per (row, group) and candidate c of ``grid``, alpha = 1 - c / (2 grid):
 //   symmetric:  s = bf16(alpha max|w| / 7), z = 8

@@ -581,6 +581,11 @@ cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st);
 
 
+// Polls of a device-side wait of the products and of the expert layer: ``most``, or fewer where
+// nq_set_w4_wait_polls set so.
+uint32_t wait_polls(uint32_t most);
+void set_wait_polls(int polls);
+
 // Many rows of X on tcgen05 (w4_tc.cu).
 struct TcPlan {
     int BN;                    // rows of X of a tile
@@ -600,6 +605,7 @@ struct MoeArgs {
     Mat gate_up;               // E matrices of 2f x d, one after the other
     Mat down;                  // E matrices of d x f
     int group;
+    uint32_t polls;            // of a wait for the other CTAs
     float *Y;                  // [B][d]
     int32_t *ids;              // [B][top_k] or null
     float *weights;            // [B][top_k] or null

@@ -18,7 +18,10 @@
 // One barrier says that a stage is full (the bytes of X and the four warps that decoded it), one
 // that it is empty.  The A operand never touches shared memory, so the MMA reads only X there.
 // The codes' pair order along k ((0,4) (1,5) (2,6) (3,7) of every 8) is that of the columns of X.
-// Every mbarrier wait is bounded; a tile whose wait ran out is stored as NaN.
+// Every mbarrier wait is bounded, and its outcome is one for the whole warp.  A role whose wait ran
+// out ends and issues nothing more; the others then run out or end in turn, and the tiles that a
+// drain did not get whole are stored as NaN.  Before such a CTA returns it waits for the copies and
+// MMAs that are still under way.
 //
 // Measured, 11008x4096 g = 128, 2048 BF16 rows: 207 us, 893 TFLOP/s, tensor pipe active 46 % of the
 // time.  What bounds it is the hand-over of stages between the roles: decoding was a good part
@@ -53,6 +56,7 @@ struct TcArgs {
     int ntiles, units;                           // tiles of X; (row tile, tile of X, part) units
     float *out;                                  // [parts][B][m]
     float out_scale;
+    uint32_t polls;                              // of a wait
 };
 struct TcMaps {
     CUtensorMap x[kTerms];
@@ -120,10 +124,15 @@ __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t
 }
 
 // One lane waits, all lanes of the warp learn the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane) {
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane, uint32_t polls) {
     int ok = 0;
-    if (lane == 0) ok = mbar_wait(bar, parity, nullptr) ? 1 : 0;
+    if (lane == 0) ok = mbar_wait(bar, parity, nullptr, polls) ? 1 : 0;
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+// All lanes wait and agree on the outcome: for the warp that issues MMAs, whose loop has to stay uniform
+// and whose issuing lane has to see the phase itself.
+__device__ __forceinline__ bool warp_wait_all(uint64_t *bar, uint32_t parity, uint32_t polls) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, nullptr, polls));
 }
 
 // Stages of the ring of codes: it runs ahead of the other one, so that codes come from memory
@@ -131,8 +140,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int la
 NQ_HD constexpr int tc_code_stages(int BN, int T) { return BN * T > 128 ? 4 : 8; }
 template <int BN, int T>
 constexpr int tc_smem() {
-    return kRing * T * BN * kStageK * 2 + tc_code_stages(BN, T) * kCodeBytes + 1024 + 256;
+    return kRing * T * BN * kStageK * 2 + tc_code_stages(BN, T) * kCodeBytes + 1024 + 512;
 }
+// What the roles leave behind for a CTA in which a wait ran out.
+struct Unfinished {
+    int lost;                                    // a wait ran out
+    uint32_t mma_groups;                         // groups whose MMAs were issued
+    uint32_t x_issued, c_issued;                 // stages of X and of codes asked for
+    uint32_t decoded[kDecodeWarps];              // stages before this one (of its turn) are decoded
+};
 
 // GS: MMA steps (16 columns of k) of a group.
 template <int BN, int T, int GS>
@@ -151,13 +167,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(codes + CODES * kCodeBytes);
     uint64_t *empty = full + kRing, *d_full = empty + kRing, *d_empty = d_full + 2,
              *c_full = d_empty + 2, *c_empty = c_full + CODES;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(c_empty + CODES);
+    uint64_t *rest = c_empty + CODES;            // the MMAs of a CTA in which a wait ran out
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rest + 1);
+    Unfinished *un = reinterpret_cast<Unfinished *>(tmem_slot + 1);
+    static_assert((2 * kRing + 4 + 2 * CODES + 1) * 8 + 4 + sizeof(Unfinished) <= 512, "barriers");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kRing; ++s) mbar_init(&full[s], 5), mbar_init(&empty[s], 1);
         for (int s = 0; s < 2; ++s) mbar_init(&d_full[s], 1), mbar_init(&d_empty[s], kDrainWarps);
         for (int s = 0; s < CODES; ++s) mbar_init(&c_full[s], 1), mbar_init(&c_empty[s], 4);
+        mbar_init(rest, 1);
+        un->lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int n0 = unit / a.parts % a.ntiles * BN;
                 for (int k = k0; k < k1; ++k, ++it) {
                     const int s = it % kRing;
-                    if (it >= kRing && !mbar_wait(&empty[s], (it / kRing - 1) & 1, nullptr)) {
+                    if (it >= kRing && !mbar_wait(&empty[s], (it / kRing - 1) & 1, nullptr, a.polls)) {
                         ok = false;
                         break;
                     }
@@ -201,6 +222,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         k * kStageK + h * BK, n0, &full[s]);
                 }
             }
+            un->x_issued = it;
+            if (!ok) un->lost = 1;
         }
     } else if (warp == 1) {
         // the whole warp walks the loop, so that the operands' addresses are uniform; one lane
@@ -215,14 +238,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             stages_of(unit, k0, k1);
             for (int k = k0; k < k1 && ok; ++k, ++it) {
                 const uint32_t s = it % kRing;
-                ok = mbar_wait(&full[s], it / kRing & 1, nullptr);
+                ok = warp_wait_all(&full[s], it / kRing & 1, a.polls);
                 if (!ok) break;
                 const uint64_t desc = desc0 + s * (STAGE / 16);
                 const uint32_t at = tmem_a + s * kStageA;
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g, ++grp) {
                     const uint32_t d = tmem + (grp & 1) * BN;
-                    if (grp >= 2) ok = mbar_wait(&d_empty[grp & 1], (grp / 2 - 1) & 1, nullptr) && ok;
+                    if (grp >= 2) ok = warp_wait_all(&d_empty[grp & 1], (grp / 2 - 1) & 1, a.polls);
+                    if (!ok) break;              // (the drain may still be reading this accumulator)
                     tc_fence_after();
                     if (leader) {
 #pragma unroll
@@ -242,6 +266,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     __syncwarp();
                 }
             }
+        }
+        if (leader) {
+            un->mma_groups = grp;
+            if (!ok) un->lost = 1;
         }
     } else if (warp < 2 + kDrainWarps) {
         // drain: rows of quarter q, columns c0 .. c0 + COLS - 1
@@ -266,7 +294,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int g = k0 * GROUPS; g < g1 && !dead; ++g, ++grp) {
                 const float s = __uint_as_float(s_next << 16);
                 s_next = __ldg(scales + min(g + 1, a.M.ng - 1));
-                if (!warp_wait(&d_full[grp & 1], grp / 2 & 1, lane)) {
+                if (!warp_wait(&d_full[grp & 1], grp / 2 & 1, lane, a.polls)) {
                     dead = true;
                     break;
                 }
@@ -292,6 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (n0 + j < a.B) dst[(int64_t)j * a.m] = f * (j & 1 ? acc[j / 2].y : acc[j / 2].x);
             }
         }
+        if (dead && lane == 0) un->lost = 1;
     } else if (warp == 2 + kDrainWarps + kDecodeWarps) {
         if (lane == 0) {
             uint32_t it = 0;
@@ -302,7 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int r0 = unit / a.parts / a.ntiles * BM;
                 for (int k = k0; k < k1; ++k, ++it) {
                     const int s = it % CODES;
-                    if (it >= CODES && !mbar_wait(&c_empty[s], (it / CODES - 1) & 1, nullptr)) {
+                    if (it >= CODES && !mbar_wait(&c_empty[s], (it / CODES - 1) & 1, nullptr, a.polls)) {
                         ok = false;
                         break;
                     }
@@ -310,6 +339,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tma_load_2d(codes + s * kCodeBytes, &maps.codes, k * (kStageK / 8), r0, &c_full[s]);
                 }
             }
+            un->c_issued = it;
+            if (!ok) un->lost = 1;
         }
     } else {
         // decode: the warps of a quarter take its stages in turn
@@ -330,8 +361,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int g = 0; g < GROUPS; ++g)
                     zv[g] = a.M.z ? __ldg(zeros + min(k * GROUPS + g, a.M.ng - 1)) : 8u;
                 const uint32_t cs = it % CODES, s = it % kRing;
-                if (!warp_wait(&c_full[cs], it / CODES & 1, lane) ||
-                    (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane))) {
+                if (!warp_wait(&c_full[cs], it / CODES & 1, lane, a.polls) ||
+                    (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane, a.polls))) {
                     ok = false;
                     break;
                 }
@@ -366,9 +397,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
+        if (lane == 0) {
+            un->decoded[warp - 2 - kDrainWarps] = it;
+            if (!ok) un->lost = 1;
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if (un->lost) {
+        // copies and MMAs that nobody waits for any more end by themselves, and their shared and
+        // tensor memory is given back after that
+        if (warp == 1) {
+            if (elect_one() && un->mma_groups > 0) {
+                mma_commit(rest);
+                mbar_wait(rest, 0, nullptr);
+            }
+            __syncwarp();
+        } else if (threadIdx.x == 0) {
+            // the last phase of each stage; decode warps that ended before it owe their arrivals
+            for (uint32_t it = un->x_issued > kRing ? un->x_issued - kRing : 0; it < un->x_issued; ++it) {
+                for (int w = 0; w < 4; ++w)
+                    if (un->decoded[4 * (it & 1) + w] <= it) mbar_arrive(&full[it % kRing]);
+                mbar_wait(&full[it % kRing], it / kRing & 1, nullptr);
+            }
+            for (uint32_t it = un->c_issued > CODES ? un->c_issued - CODES : 0; it < un->c_issued; ++it)
+                mbar_wait(&c_full[it % CODES], it / CODES & 1, nullptr);
+        }
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
@@ -443,6 +499,7 @@ cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *x
     a.units = (int)ceil_div(m, BM) * a.ntiles * p.parts;
     a.out = p.parts > 1 ? partial : Y;
     a.out_scale = p.parts > 1 ? 1.f : kCodeUnit;
+    a.polls = wait_polls(kMbarSpinLimit);
     cudaError_t e;
     if (terms == 1)
         e = p.BN == 32    ? tc_launch<32, 1>(maps, a, group, st)
