@@ -385,7 +385,7 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
  * any other sum whose value is in range; results below 2^-115 are rounded to multiples of 2^-138.
  * An infinite or NaN activation reaches its own row of Y
  * alone, a scale that is not finite its own column; should a device-side wait of a many-row call run
- * out, what it kept from being computed is NaN in Y.  Up to 16 columns (BF16 rows of X, or FP32
+ * out, what it kept from being computed is NaN in Y (nq_w4_check).  Up to 16 columns (BF16 rows of X, or FP32
  * ones three each) run on warp-level MMAs that read the codes once; more on tcgen05 with the
  * decoded codes as an operand in tensor memory.  The codes of zeros past 15 count by their
  * low four bits.  Enqueue only.
@@ -393,6 +393,12 @@ size_t nq_w4_workspace_size(int64_t m, int64_t n, nq_dtype dt, int64_t B);
 nq_status nq_w4_matmul(const uint32_t *packed, const void *scales, const uint8_t *zeros, int64_t m,
                        int64_t n, int32_t group, const void *X, nq_dtype dt, int64_t B, float *Y,
                        void *ws, size_t ws_bytes, nq_stream_t stream);
+
+/* Device error word that a call of nq_w4_matmul with these sizes left in its workspace: NQ_OK, or
+ * NQ_ERR_TIMEOUT if a device-side wait ran out (some of Y is NaN).  The next call clears it.  NQ_OK for
+ * sizes whose calls have no such waits.  Synchronises the stream. */
+nq_status nq_w4_check(int64_t m, int64_t n, nq_dtype dt, int64_t B, void *ws, size_t ws_bytes,
+                      nq_stream_t stream);
 
 /* Limits of nq_moe_w4. */
 #define NQ_MOE_MAX_TOKENS 64
@@ -417,7 +423,7 @@ size_t nq_moe_workspace_size(int64_t B, int64_t d, int64_t f, int32_t E, int32_t
  * Logits are summed in FP64; products as in nq_w4_matmul; the activated rows are FP32; y is
  * summed in the order of ids.  A token's result does not depend on the others of the call.
  * Two launches: the logits, and one cooperative kernel for the rest (its grid-wide waits are
- * bounded; should one run out, Y is NaN).  Sizes: 1 <= d, f <= 65536,
+ * bounded; should one run out, what it kept from being computed is NaN: nq_moe_check).  Sizes: 1 <= d, f <= 65536,
  * 1 <= top_k <= min(E, NQ_MOE_MAX_TOP_K), E <= NQ_MOE_MAX_EXPERTS, E 2f and E d <= 2^24
  * (NQ_ERR_INVALID_ARG otherwise).  Enqueue only.
  */
@@ -427,6 +433,10 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
                     const void *down_scales, const uint8_t *down_zeros, int64_t f, int32_t group,
                     float *Y, int32_t *ids, float *weights, void *ws, size_t ws_bytes,
                     nq_stream_t stream);
+
+/* The same for nq_moe_w4. */
+nq_status nq_moe_check(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k, nq_dtype dt, void *ws,
+                       size_t ws_bytes, nq_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
 /* Step-level interface over the ADMM state held in the workspace.             */

@@ -24,6 +24,7 @@ __all__ = [
     "nq_bpw", "nq_rank_for_bpw", "nq_calib_stats", "nq_calib_precond", "nq_lbadmm",
     "nq_recon_error", "nq_pack_signs", "nq_binary_matmul", "nq_ls_refit", "LBState", "NQError",
     "status_string", "lib", "nq_w4_quantize", "nq_w4_dequantize", "nq_w4_matmul", "nq_moe_w4",
+    "nq_w4_check", "nq_moe_check",
     "nq_launch_count", "nq_profile_enable", "nq_profile_get", "nq_selftest",
     "nq_set_inverse_mode", "nq_set_tuning", "nq_set_latent_solver", "nq_set_w4_wait_polls",
 ]
@@ -324,6 +325,29 @@ def nq_moe_w4(X, router, gate_up, gate_up_scales, down, down_scales, top_k, grou
              group, Y.data_ptr(), None if ids is None else ids.data_ptr(),
              None if weights is None else weights.data_ptr(), ws_ptr, ws_bytes)
     return (Y, ids, weights) if want_routing else Y
+
+
+def _w4_status(fn, ws, *sizes):
+    """Status word that a call left in the workspace ``ws``."""
+    if not (ws.is_cuda and ws.is_contiguous() and ws.element_size() == 1):
+        raise ValueError("ws must be a contiguous CUDA byte tensor")
+    dev = ws.get_device()
+    with torch.cuda.device(dev):
+        code = fn(*sizes, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if code not in (_lib.NQ_OK, _lib.NQ_ERR_TIMEOUT):
+        raise NQError(fn.__name__, code)
+    return code
+
+
+def nq_w4_check(m, n, dtype, B, ws):
+    """What a call of nq_w4_matmul with these sizes left in its workspace: 0, or NQ_ERR_TIMEOUT if a
+    device-side wait ran out (some of its output is NaN).  Synchronises the stream."""
+    return _w4_status(lib.nq_w4_check, ws, m, n, _DTYPES[dtype], B)
+
+
+def nq_moe_check(B, d, f, E, top_k, dtype, ws):
+    """The same for nq_moe_w4."""
+    return _w4_status(lib.nq_moe_check, ws, B, d, f, E, top_k, _DTYPES[dtype])
 
 
 def nq_set_inverse_mode(mode):

@@ -68,6 +68,8 @@ SIGNATURES = {
     "nq_moe_workspace_size": (c_sz, [c_i64, c_i64, c_i64, c_i32, c_i32, c_i32]),
     "nq_moe_w4": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp,
                           c_vp, c_vp, c_vp, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "nq_w4_check": (c_i32, [c_i64, c_i64, c_i32, c_i64, c_vp, c_sz, c_vp]),
+    "nq_moe_check": (c_i32, [c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_vp, c_sz, c_vp]),
     "nq_set_w4_wait_polls": (c_i32, [c_i32]),
     "nq_lbadmm_prepare": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_vp, c_vp, c_i32, c_u64, c_i32,
                                   c_vp, c_vp, c_sz, c_vp]),

@@ -1449,7 +1449,7 @@ struct MoeLayout {
             off = align_up(off + bytes);
             return o;
         };
-        bar = take(2 * sizeof(unsigned int));
+        bar = take(3 * sizeof(unsigned int));
         logits = take((size_t)ceil_div(d, 1024) * B * E * 8);
         xw = take((size_t)B * (dt == NQ_BF16 ? 1 : w4::kTerms) * w4::padded(d) * 2);
         h = take((size_t)B * top_k * w4::kTerms * w4::padded(f) * 2);
@@ -1501,6 +1501,7 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     a.ids = ids;
     a.weights = weights;
     a.bar = at<unsigned int>(ws, L.bar);
+    a.err = reinterpret_cast<int *>(a.bar + 2);
     a.logits = at<double>(ws, L.logits);
     a.xw = at<uint4>(ws, L.xw);
     a.h = at<__nv_bfloat16>(ws, L.h);
@@ -1508,6 +1509,30 @@ nq_status nq_moe_w4(const void *X, nq_dtype dt, int64_t B, int64_t d, const void
     ProfScope ps(NQ_K_MOE, cs(stream));
     NQ_CK(w4::moe(a, cs(stream)));
     return NQ_OK;
+}
+
+nq_status nq_w4_check(int64_t m, int64_t n, nq_dtype dt, int64_t B, void *ws, size_t ws_bytes,
+                      nq_stream_t stream) {
+    const size_t need = nq_w4_workspace_size(m, n, dt, B);
+    if (!need) {
+        const bool sizes = m >= 1 && n >= 1 && B >= 1 && m <= w4::kMaxRows && n <= kMaxDim &&
+                           B <= kMaxDim && dtype_ok(dt);
+        return sizes ? NQ_OK : NQ_ERR_INVALID_ARG;      // (a call without a workspace has no waits)
+    }
+    if (nq_status st = check_ws(ws, ws_bytes, need)) return st;
+    const size_t word = w4::matmul_error_word(m, n, dt == NQ_BF16, B);
+    if (!word) return NQ_OK;
+    if (nq_status st = check_device()) return st;
+    return read_err(at<int>(ws, word), cs(stream), false);
+}
+
+nq_status nq_moe_check(int64_t B, int64_t d, int64_t f, int32_t E, int32_t top_k, nq_dtype dt, void *ws,
+                       size_t ws_bytes, nq_stream_t stream) {
+    if (!moe_sizes_ok(B, d, f, E, top_k) || !dtype_ok(dt)) return NQ_ERR_INVALID_ARG;
+    const MoeLayout L(B, d, f, E, top_k, dt);
+    if (nq_status st = check_ws(ws, ws_bytes, L.total)) return st;
+    if (nq_status st = check_device()) return st;
+    return read_err(at<int>(ws, L.bar + 2 * sizeof(unsigned int)), cs(stream), false);
 }
 
 nq_status nq_set_w4_wait_polls(int32_t polls) {

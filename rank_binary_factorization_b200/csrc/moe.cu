@@ -24,8 +24,8 @@ constexpr int kRouterColumns = 8 * kRouterThreads;
 // ---- router logits, columns of X --------------------------------------------------------
 // CTA: one expert, up to 8 tokens, 1024 columns; the sums are in FP64 (the parts of a logit are
 // added up by ``choose``), so that which experts are chosen does not depend on their order.  The
-// CTAs together also write X's columns in word order and clear the arrival counts of the kernel
-// that follows.
+// CTAs together also write X's columns in word order and clear the arrival counts and the error
+// word of the kernel that follows.
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, int left, bool vec, T (&v)[8]) {
     if (vec && left >= 8) {
@@ -51,7 +51,10 @@ __global__ void __launch_bounds__(kRouterThreads) moe_logits_kernel(const MoeArg
 #pragma unroll
     for (int b = 0; b < kRouterTokens; ++b)
         if (b < nb) load8(X + (int64_t)(b0 + b) * a.d + k, left, vec, x[b]);
-    if (e == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < 2) a.bar[threadIdx.x] = 0;
+    if (e == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+        if (threadIdx.x < 2) a.bar[threadIdx.x] = 0;
+        if (threadIdx.x == 2) *a.err = 0;
+    }
     const int words = (int)(padded(a.d) / 8);
     const int ctas = gridDim.x * gridDim.y * gridDim.z,
               cta = (blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
@@ -235,9 +238,12 @@ __device__ __forceinline__ void arrive(unsigned int *bar) {
     __syncthreads();
     if (threadIdx.x == 0) release_add(bar, 1);
 }
-__device__ __forceinline__ bool all_arrived(unsigned int *bar, uint32_t polls) {
+__device__ __forceinline__ bool all_arrived(unsigned int *bar, const MoeArgs &a) {
     bool ok = true;
-    if (threadIdx.x == 0) ok = wait_geq(bar, gridDim.x, polls);
+    if (threadIdx.x == 0) {
+        ok = wait_geq(bar, gridDim.x, a.polls);
+        if (!ok) raise_error(a.err, NQ_ERR_TIMEOUT);
+    }
     return __syncthreads_and(ok);
 }
 
@@ -349,7 +355,7 @@ struct DownProb : ExpertJobs {
         return (expert(c) + 1) * a.d - 1;
     }
     // the first copies of the weights are under way; h is complete when all CTAs have arrived
-    __device__ __forceinline__ void ready() { ok = all_arrived(a.bar, a.polls); }
+    __device__ __forceinline__ void ready() { ok = all_arrived(a.bar, a); }
     __device__ __forceinline__ const char *col(const Cursor &cur, int j, bool &odd) const {
         int pair, term;
         column(cur, j, pair, term);
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2) moe_experts_kernel(const MoeAr
     }
     __threadfence();
     arrive(a.bar + 1);
-    ok = all_arrived(a.bar + 1, a.polls) && ok;
+    ok = all_arrived(a.bar + 1, a) && ok;
     const int64_t count = (int64_t)a.B * a.d;
     for (int64_t o = (int64_t)blockIdx.x * 32 * kWarps + threadIdx.x; o < count;
          o += (int64_t)gridDim.x * 32 * kWarps) {

@@ -557,9 +557,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 }
 
 // X (B x n) as columns: [B][1 or kTerms][padded(n)], the words of a half placed for VW.
+// err: an error word to clear, or null.
 template <int VW>
 __global__ void __launch_bounds__(256)
-    x_words_kernel(const void *X, int x_bf16, int64_t B, int n, uint4 *__restrict__ xw) {
+    x_words_kernel(const void *X, int x_bf16, int64_t B, int n, uint4 *__restrict__ xw, int *err) {
+    if (err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *err = 0;
     const int words = (int)(padded(n) / 8);
     const int64_t b = blockIdx.x;
     const int wd = blockIdx.y * blockDim.x + threadIdx.x;
@@ -597,10 +599,17 @@ static size_t x_bytes(int64_t n, int x_bf16, int64_t B) {
     return (b + 255) / 256 * 256;
 }
 
+// Workspace: the columns of X and, on the tensor-memory path, the parts' sums and the error word.
 size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B) {
     if (x_shared(n, x_bf16, B)) return 0;
-    const size_t x = x_bytes(n, x_bf16, B);
-    return on_tensor_memory(x_bf16, B) ? x + tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes : x;
+    if (!on_tensor_memory(x_bf16, B)) return x_bytes(n, x_bf16, B);
+    return matmul_error_word(m, n, x_bf16, B) + sizeof(int);
+}
+
+size_t matmul_error_word(int64_t m, int64_t n, int x_bf16, int64_t B) {
+    if (!on_tensor_memory(x_bf16, B)) return 0;
+    const size_t b = x_bytes(n, x_bf16, B) + tc_plan(m, n, x_bf16 ? 1 : kTerms, B).partial_bytes;
+    return (b + 255) / 256 * 256;
 }
 
 template <int VW, bool Z, bool SV, bool XS, int MT, int NT>
@@ -645,19 +654,21 @@ static cudaError_t gemv(const Mat &M, int64_t m, const void *X, int x_bf16, cons
 
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st) {
+    char *ws = reinterpret_cast<char *>(xw);
+    int *err = on_tensor_memory(x_bf16, B)
+                   ? reinterpret_cast<int *>(ws + matmul_error_word(m, M.n, x_bf16, B)) : nullptr;
     if (!x_shared(M.n, x_bf16, B)) {
         auto words = on_tensor_memory(x_bf16, B) ? x_words_kernel<0>
                      : group == 32 ? x_words_kernel<1>
                      : group == 64 ? x_words_kernel<2>
                                    : x_words_kernel<4>;
         words<<<dim3((unsigned)B, (unsigned)ceil_div(padded(M.n) / 8, 256)), 256, 0, st>>>(
-            X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw));
+            X, x_bf16, B, M.n, reinterpret_cast<uint4 *>(xw), err);
         count_launch();
     }
     if (on_tensor_memory(x_bf16, B))
         return tc_matmul(M, m, group, xw, x_bf16 ? 1 : kTerms, B, Y,
-                         reinterpret_cast<float *>(reinterpret_cast<char *>(xw) + x_bytes(M.n, x_bf16, B)),
-                         st);
+                         reinterpret_cast<float *>(ws + x_bytes(M.n, x_bf16, B)), err, st);
     auto run = M.z ? (group == 32 ? gemv<1, true> : group == 64 ? gemv<2, true> : gemv<4, true>)
                    : (group == 32 ? gemv<1, false> : group == 64 ? gemv<2, false> : gemv<4, false>);
     return run(M, m, X, x_bf16, xw, B, Y, st);

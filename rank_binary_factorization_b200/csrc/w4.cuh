@@ -574,9 +574,11 @@ cudaError_t quantize(const void *W, int w_bf16, int64_t m, int64_t n, const floa
                      int grid, uint32_t *q, __nv_bfloat16 *s, uint8_t *z, cudaStream_t st);
 cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf16,
                        cudaStream_t st);
-// xw: workspace (matmul_workspace bytes) for the columns of X in word order and the parts of a
-// split k axis.
+// xw: workspace (matmul_workspace bytes) for the columns of X in word order, the parts of a split k
+// axis and an error word.
 size_t matmul_workspace(int64_t m, int64_t n, int x_bf16, int64_t B);
+// Place of the error word in it; 0 where the call has none (no waits).
+size_t matmul_error_word(int64_t m, int64_t n, int x_bf16, int64_t B);
 cudaError_t matmul(const Mat &M, int64_t m, int group, const void *X, int x_bf16, int64_t B,
                    float *Y, __nv_bfloat16 *xw, cudaStream_t st);
 
@@ -594,7 +596,7 @@ struct TcPlan {
 };
 TcPlan tc_plan(int64_t m, int64_t n, int terms, int64_t B);
 cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *xw, int terms, int64_t B,
-                      float *Y, float *partial, cudaStream_t st);
+                      float *Y, float *partial, int *err, cudaStream_t st);
 
 // Expert layer for a few tokens (moe.cu).
 struct MoeArgs {
@@ -611,6 +613,7 @@ struct MoeArgs {
     float *weights;            // [B][top_k] or null
     // workspace
     unsigned int *bar;         // two arrival counts
+    int *err;                  // error word (behind the counts)
     double *logits;            // [ceil(d / 1024)][B][E]: parts of a logit
     uint4 *xw;                 // [B][1 or kTerms][padded(d) / 8], word order
     __nv_bfloat16 *h;          // [B top_k][kTerms][padded(f)], word order

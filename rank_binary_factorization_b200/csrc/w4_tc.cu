@@ -57,6 +57,7 @@ struct TcArgs {
     float *out;                                  // [parts][B][m]
     float out_scale;
     uint32_t polls;                              // of a wait
+    int *err;                                    // NQ_ERR_TIMEOUT where one ran out
 };
 struct TcMaps {
     CUtensorMap x[kTerms];
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (un->lost) {
+        if (threadIdx.x == 0) raise_error(a.err, NQ_ERR_TIMEOUT);
         // copies and MMAs that nobody waits for any more end by themselves, and their shared and
         // tensor memory is given back after that
         if (warp == 1) {
@@ -481,7 +483,7 @@ static cudaError_t tc_launch(const TcMaps &maps, const TcArgs &a, int group, cud
 }
 
 cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *xw, int terms, int64_t B,
-                      float *Y, float *partial, cudaStream_t st) {
+                      float *Y, float *partial, int *err, cudaStream_t st) {
     const TcPlan p = tc_plan(m, M.n, terms, B);
     const int64_t ldx = padded(M.n);
     TcMaps maps;
@@ -500,6 +502,7 @@ cudaError_t tc_matmul(const Mat &M, int64_t m, int group, const __nv_bfloat16 *x
     a.out = p.parts > 1 ? partial : Y;
     a.out_scale = p.parts > 1 ? 1.f : kCodeUnit;
     a.polls = wait_polls(kMbarSpinLimit);
+    a.err = err;
     cudaError_t e;
     if (terms == 1)
         e = p.BN == 32    ? tc_launch<32, 1>(maps, a, group, st)
