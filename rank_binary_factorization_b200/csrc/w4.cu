@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(256)
     const float s = __bfloat162float(M.s[at]);
     // the code in the low mantissa bits of 2^23
     const float off = 8388608.f + (M.z ? (float)(__ldg(M.z + at) & 15) : 8.f);
-    T v[kPer];
+    __align__(16) T v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const uint32_t c = ((i < 8 ? w.x : w.y) >> (4 * (i & 7))) & 15u;
