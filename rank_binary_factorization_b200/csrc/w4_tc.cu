@@ -124,15 +124,10 @@ __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t
     acc = *reinterpret_cast<float2 *>(&a);
 }
 
-// One lane waits, all lanes of the warp learn the outcome.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int lane, uint32_t polls) {
-    int ok = 0;
-    if (lane == 0) ok = mbar_wait(bar, parity, nullptr, polls) ? 1 : 0;
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
-// All lanes wait and agree on the outcome: for the warp that issues MMAs, whose loop has to stay uniform
-// and whose issuing lane has to see the phase itself.
-__device__ __forceinline__ bool warp_wait_all(uint64_t *bar, uint32_t parity, uint32_t polls) {
+// All lanes of the warp wait, and agree on the outcome.  Each sees the phase itself: what one lane saw,
+// handed on by a shuffle, would not order the others' reads behind the wait.  (Faster, too: 11008x4096
+// g = 32, 2048 rows 543 -> 474 us, 28672x8192, 32 rows 67 -> 60 us.)
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t polls) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, nullptr, polls));
 }
 
@@ -239,14 +234,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             stages_of(unit, k0, k1);
             for (int k = k0; k < k1 && ok; ++k, ++it) {
                 const uint32_t s = it % kRing;
-                ok = warp_wait_all(&full[s], it / kRing & 1, a.polls);
+                ok = warp_wait(&full[s], it / kRing & 1, a.polls);
                 if (!ok) break;
                 const uint64_t desc = desc0 + s * (STAGE / 16);
                 const uint32_t at = tmem_a + s * kStageA;
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g, ++grp) {
                     const uint32_t d = tmem + (grp & 1) * BN;
-                    if (grp >= 2) ok = warp_wait_all(&d_empty[grp & 1], (grp / 2 - 1) & 1, a.polls);
+                    if (grp >= 2) ok = warp_wait(&d_empty[grp & 1], (grp / 2 - 1) & 1, a.polls);
                     if (!ok) break;              // (the drain may still be reading this accumulator)
                     tc_fence_after();
                     if (leader) {
@@ -295,7 +290,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int g = k0 * GROUPS; g < g1 && !dead; ++g, ++grp) {
                 const float s = __uint_as_float(s_next << 16);
                 s_next = __ldg(scales + min(g + 1, a.M.ng - 1));
-                if (!warp_wait(&d_full[grp & 1], grp / 2 & 1, lane, a.polls)) {
+                if (!warp_wait(&d_full[grp & 1], grp / 2 & 1, a.polls)) {
                     dead = true;
                     break;
                 }
@@ -362,8 +357,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int g = 0; g < GROUPS; ++g)
                     zv[g] = a.M.z ? __ldg(zeros + min(k * GROUPS + g, a.M.ng - 1)) : 8u;
                 const uint32_t cs = it % CODES, s = it % kRing;
-                if (!warp_wait(&c_full[cs], it / CODES & 1, lane, a.polls) ||
-                    (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, lane, a.polls))) {
+                if (!warp_wait(&c_full[cs], it / CODES & 1, a.polls) ||
+                    (it >= kRing && !warp_wait(&empty[s], (it / kRing - 1) & 1, a.polls))) {
                     ok = false;
                     break;
                 }
