@@ -327,13 +327,16 @@ def nq_moe_w4(X, router, gate_up, gate_up_scales, down, down_scales, top_k, grou
     return (Y, ids, weights) if want_routing else Y
 
 
-def _w4_status(fn, ws, *sizes):
-    """Status word that a call left in the workspace ``ws``."""
+def _w4_status(fn, ws, dtype, *sizes):
+    """Status word that a call on inputs of ``dtype`` left in the workspace ``ws``."""
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"unsupported dtype {dtype}: use float32 or bfloat16")
     if not (ws.is_cuda and ws.is_contiguous() and ws.element_size() == 1):
         raise ValueError("ws must be a contiguous CUDA byte tensor")
     dev = ws.get_device()
     with torch.cuda.device(dev):
-        code = fn(*sizes, ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        code = fn(*(dt if v is dtype else v for v in sizes), ws.data_ptr(), ws.numel(), _raw_stream(dev))
     if code not in (_lib.NQ_OK, _lib.NQ_ERR_TIMEOUT):
         raise NQError(fn.__name__, code)
     return code
@@ -342,12 +345,12 @@ def _w4_status(fn, ws, *sizes):
 def nq_w4_check(m, n, dtype, B, ws):
     """What a call of nq_w4_matmul with these sizes left in its workspace: 0, or NQ_ERR_TIMEOUT if a
     device-side wait ran out (some of its output is NaN).  Synchronises the stream."""
-    return _w4_status(lib.nq_w4_check, ws, m, n, _DTYPES[dtype], B)
+    return _w4_status(lib.nq_w4_check, ws, dtype, m, n, dtype, B)
 
 
 def nq_moe_check(B, d, f, E, top_k, dtype, ws):
     """The same for nq_moe_w4."""
-    return _w4_status(lib.nq_moe_check, ws, B, d, f, E, top_k, _DTYPES[dtype])
+    return _w4_status(lib.nq_moe_check, ws, dtype, B, d, f, E, top_k, dtype)
 
 
 def nq_set_inverse_mode(mode):

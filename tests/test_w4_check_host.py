@@ -36,3 +36,11 @@ def test_wrappers_refuse_a_workspace_on_the_host():
         nq.nq_w4_check(64, 64, torch.float32, 99, ws)
     with pytest.raises(ValueError):
         nq.nq_moe_check(1, 64, 32, 4, 2, torch.float32, ws)
+
+
+def test_wrappers_refuse_other_types():
+    ws = torch.empty(1024, dtype=torch.uint8)
+    with pytest.raises(TypeError):
+        nq.nq_w4_check(64, 64, torch.float16, 99, ws)
+    with pytest.raises(TypeError):
+        nq.nq_moe_check(1, 64, 32, 4, 2, torch.int8, ws)
