@@ -327,17 +327,19 @@ nq_status nq_binary_matmul(const uint32_t *U_packed, const uint32_t *V_packed, c
                            nq_stream_t stream);
 
 /* ------------------------------------------------------------------------- */
-/* 4. Layers with 4-bit weights.  Below one bit is not for every layer (summary */
-/* page, "Limitations" (局限与改进)): heads, sensitive projections and experts    */
-/* are kept at 4 bits beside the binary factors, quantised with the same         */
-/* calibration (d_in) and applied to one token or to a prompt.                   */
+/* 4. Layers with 4-bit weights.  An addition of this library, not a step of the  */
+/* pages, where every layer has one uniform rank and none is kept at 4 bits: its   */
+/* reading of their limitations (summary page, 局限与改进) is that heads, sensitive */
+/* projections and experts need more than one bit.  They are quantised with the    */
+/* same calibration (d_in) and applied to one token or to a prompt.                */
 /*                                                                               */
 /* Format of an m x n layer with group size g (32, 64 or 128):                    */
 /*   packed uint32 [m][4 ceil(n/32)]: the code q of column k is nibble k % 8      */
 /*     (lowest first) of word k / 8 of its row; codes past column n are ignored;   */
 /*   scales bf16 [m][ceil(n/g)]; zeros uint8 [m][ceil(n/g)] (0..15), or NULL for   */
 /*     a zero point of 8 everywhere;                                              */
-/*   W^[i][k] = scale (q - zero), exact in FP32.                                  */
+/*   W^[i][k] = scale (q - zero), exact in FP32 (read back as infinite where that is */
+/*     past FP32's range, as a scale rounded up brings about for weights next to it). */
 /* Supported sizes: 1 <= n <= 65536, 1 <= m <= 2^24 (a stack of layers is one      */
 /* array of rows).  packed starts on a 16-byte boundary.                           */
 /* ------------------------------------------------------------------------- */

@@ -5,12 +5,15 @@
 //
 // Two launches: the logits, then one cooperative kernel for the choice, both products and the
 // sum, whose CTAs wait for one another twice (the down product needs all of h, the sum all parts).
-// An expert's rows are read once for all tokens that chose it.  Measured, bf16 unless said: one
-// token, 64 experts, top 6, 2048 x 1408: 27 us (latency: the choice, two grid waits, about one job
-// a CTA in each product); 8 tokens, 64 experts, top 8, 4096 x 1024, g = 64 with zero points:
-// 115 us, 290 MB (39 % of the copy rate, 59 % of the issue slots: decoding and the joins of jobs);
-// 16 tokens, 8 experts, top 2, 4096 x 11008, FP32: 279 us (three columns a token to multiply).
-// With a launch for each step: 84, 315, 580 us.
+// An expert's rows are read once for all tokens that chose it (FP32: for every five).  Measured, bf16
+// unless said: one token, 64 experts, top 6, 2048 x 1408: 27 us (latency: the choice, two grid waits,
+// about one job a CTA in each product); 8 tokens, 64 experts, top 8, 4096 x 1024, g = 64 with zero
+// points: 115 us, 290 MB (39 % of the copy rate, 59 % of the issue slots, 1.2 warps eligible a
+// scheduler, so neither is used up: a warp's chain of copy, decode, MMA, and the joins of jobs);
+// 16 tokens, 8 experts, top 2, 4096 x 11008, FP32: 278 us (three columns a token to multiply; every
+// FP32 variant spills, 76 to 704 bytes of stores at 128 registers, and 0.8 warps are eligible).
+// With a launch for each step: 84, 315, 580 us.  Gate and up jobs go up to padded(f) rows: the blocks
+// past f (4 of 48 at f = 1408) work on the last row again and store the zeros of h's padding.
 #include "w4.cuh"
 
 namespace nq {
@@ -327,7 +330,7 @@ struct GateUpProb : ExpertJobs {
         const int r0 = (cur.block << lrows) + 16 * wr, np = pairs(cur), p0 = L.chunk_first[cur.chunk];
         for (int o = threadIdx.x - wr * 32 * WK; o < 16 * np; o += 32 * WK) {
             const int r = o % 16, p = o / 16, k = r0 + r;
-            if (k >= ldh) continue;
+            if (k >= ldh) continue;              // (never: blocks divide it; without, one variant spills more)
             const float g = R.sum(wr, WK, r, p * terms, terms),
                         u = R.sum(wr, WK, 16 + r, p * terms, terms);
             __nv_bfloat16 ht[kTerms];

@@ -30,9 +30,10 @@ void set_wait_polls(int polls) { g_wait_polls.store(polls, std::memory_order_rel
 // them anew (about one comparison in 10000).
 //
 // Measured: 4096x4096 BF16, g = 128, 16 candidates 93 us, twice the 44 us that the search's FMA-pipe
-// operations take at full rate: latency and issue (shuffles, sums across a group's lanes, the settled
-// pairs) bound it.  28672x8192 BF16, g = 64, zero points, one candidate: 137 us, 598 MB, 68 % of the
-// copy rate, bound by issue (a rounded quotient for every column); FP32, g = 32: 186 us, 90 %, bound by
+// operations take at full rate: the rest is latency and issue (shuffles, sums across a group's lanes,
+// the settled pairs; 24 bytes of spills at the 64 registers of four CTAs an SM).  28672x8192 BF16,
+// g = 64, zero points, one candidate: 137 us, 598 MB, 68 % of the copy rate at 68 % of the issue slots
+// (a rounded quotient for every column): neither is used up; FP32, g = 32: 186 us, 90 %, bound by
 // memory.  The correction of the quotient instead of a settled remainder for every column:
 // 614 -> 190 us; two columns an operation and 32 a lane: 184 -> 137 us.
 // ---------------------------------------------------------------------------------
@@ -111,7 +112,9 @@ __device__ __forceinline__ T group_sum(T v) {
 }
 
 // x / c in FP64 for a quotient far from the ends of its range, r about 1 / c: the residual of
-// the first quotient is exact and corrects it to the rounded one.
+// the first quotient is exact and corrects it to the rounded one (Markstein's correction: P. W.
+// Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34, 1990).
 __device__ __forceinline__ double quotient(double x, double c, double r) {
     const double q = x * r;
     return fma(fma(-q, c, x), r, q);
@@ -437,8 +440,10 @@ cudaError_t dequantize(const Mat &M, int64_t m, int group, void *out, int out_bf
 // ---------------------------------------------------------------------------------
 // Matrix product for few columns: persistent CTAs, two an SM, walk the row tiles (run_products).
 // Measured: 4096x4096 g = 128, one BF16 row of X 6.4 us (latency: prologue, one job a CTA, the
-// join); 11008x4096 g = 64 with zero points 11.5 us; 28672x8192 g = 128, 16 rows of X 52 us (the
-// columns, 256 KB, come through L1 and L2 for every job).
+// join); 11008x4096 g = 64 with zero points 11.5 us; 28672x8192 g = 128, 16 rows of X 51-53 us (the
+// columns, 256 KB, come through L1 and L2 for every job, and the variant spills).  Above n = 9216 for
+// one BF16 row the columns are laid out in global memory by a launch of their own: 4096x11008 12 us,
+// 8192x28672 33 us.
 // ---------------------------------------------------------------------------------
 template <int VW, int MT, int NT, bool XS>
 struct GemvProb {
@@ -581,8 +586,9 @@ __global__ void __launch_bounds__(256)
 }
 
 // Columns of the call above which the tensor-memory path (w4_tc.cu) takes it: the most that this
-// one holds at a time.  28672x8192: 16 BF16 rows 51 us here, 17 there 65; 8 FP32 rows (24 columns,
-// the codes twice) 85 us here, 67 there.  4096x4096, 8 FP32 rows: 12.1 here, 13.3 there.
+// one holds at a time, whatever m and n are.  28672x8192: 16 BF16 rows 51-53 us here, 17 there 57; 8
+// FP32 rows (24 columns, the codes twice) 85 us here, 67 there.  4096x4096: 16 BF16 rows 9.7 us here, 17
+// there 12.1; 8 FP32 rows 12.1 here, 11.7 there.
 constexpr int kMaxColumns = 16;
 static bool on_tensor_memory(int x_bf16, int64_t B) {
     return B * (x_bf16 ? 1 : kTerms) > kMaxColumns;

@@ -179,8 +179,10 @@ NQ_HD int in_word(int k) { return (k & ~7) | (k & 3) << 1 | (k >> 2 & 1); }
 //
 // Measured, 28672x8192 g = 128, one BF16 column: 32 us, 3.8 TB/s (58 % of the copy rate); 162
 // instructions for 16 rows x 128 columns, 57 % of the issue slots, 100 registers, two CTAs an SM.
-// Decoding (one shift, four logical operations and four FMAs for 8 codes, then the MMA and the
-// group's scale) bounds it with the latency of a warp's own chain: copy, decode, MMA.
+// Neither memory nor issue is used up: of 3.6 warps a scheduler 1.2 are eligible, too few in flight
+// for a warp's own chain (copy, decode, MMA, scale).  Two row tiles by two column tiles, for 9 to 16
+// columns that do not fit shared memory, need more than the 128 registers that two CTAs leave: their
+// variants spill 28 to 708 bytes of stores (28672x8192, 16 rows: 28 bytes, 0.9 warps eligible).
 //
 // Prob supplies: jobs, a Cursor over them with first() and next(cursor), first_row(cursor, group,
 // tile) and last_row(cursor, tile) -> rows of M, col(cursor, j, odd) -> the lane's column of n-tile

@@ -23,12 +23,15 @@
 // drain did not get whole are stored as NaN.  Before such a CTA returns it waits for the copies and
 // MMAs that are still under way.
 //
-// Measured, 11008x4096 g = 128, 2048 BF16 rows: 207 us, 893 TFLOP/s, tensor pipe active 46 % of the
-// time.  What bounds it is the hand-over of stages between the roles: decoding was a good part
-// while one warp a quarter of the rows did it (239 us; 204 us in a copy with the decoding left
-// out), two of them, stages in turn, brought it to 207 us.  Before: 64 columns a stage and a ring
-// for each operand 549 us, four drain warps instead of eight 271 us.  At g = 32 the drain, four
-// a stage, bounds it.
+// Measured, 11008x4096 g = 128, 2048 BF16 rows: 191 us, 964 TFLOP/s in a graph of 24 calls after a
+// pause; 216 us in a run of seconds, under the power cap at a median of 1690 MHz.  The tensor pipe
+// is active 51 % of the time and 63 % of the issue slots are used, the polls of waits among them; no
+// unit is used up, and what is left is the hand-over of stages between the roles and the decoding of
+// a row tile's codes for every 128 rows of X.  Decoding was a good part while one warp a quarter of the
+// rows did it (239 us; 204 us in a copy with the decoding left out), two of them, stages in turn,
+// brought it to 207 us.  Before: 64 columns a stage and a ring for each operand 549 us, four drain
+// warps instead of eight 271 us.  g = 64: 277 us, g = 32: 474 us, with two and four drains a stage.
+// FP32, 512 rows: 119 us (64 rows of X a tile, three terms each).
 #include "gemm_tc.cuh"
 #include "tc_ptx.cuh"
 #include "w4.cuh"
@@ -126,7 +129,7 @@ __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t
 
 // All lanes of the warp wait, and agree on the outcome.  Each sees the phase itself: what one lane saw,
 // handed on by a shuffle, would not order the others' reads behind the wait.  (Faster, too: 11008x4096
-// g = 32, 2048 rows 543 -> 474 us, 28672x8192, 32 rows 67 -> 60 us.)
+// g = 32, 2048 rows 543 -> 474 us, 28672x8192, 32 rows 66 -> 58 us.)
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint32_t polls) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, nullptr, polls));
 }
